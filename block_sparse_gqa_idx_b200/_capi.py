@@ -9,7 +9,9 @@ module raises at import: there is no other implementation to fall back to.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
 import os
 from typing import Optional, Tuple
 
@@ -58,6 +60,12 @@ class msa_proj_dims(ctypes.Structure):
                 ("H_kv", ctypes.c_int32), ("d_h", ctypes.c_int32), ("d_idx", ctypes.c_int32)]
 
 
+class msa_norm_rope_dims(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("H_q", ctypes.c_int32), ("H_k", ctypes.c_int32),
+                ("d", ctypes.c_int32), ("rot", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("eps", ctypes.c_float)]
+
+
 class msa_kernel_time(ctypes.Structure):
     _fields_ = [("name", ctypes.c_char * 48), ("launches", ctypes.c_int32),
                 ("total_ms", ctypes.c_double)]
@@ -73,7 +81,8 @@ EXPORTS = ("msa_index_topk_workspace", "msa_index_topk", "msa_sparse_attn_fwd_wo
            "msa_index_topk_varlen_workspace", "msa_index_topk_varlen",
            "msa_sparse_attn_fwd_varlen_workspace", "msa_sparse_attn_fwd_varlen",
            "msa_project_workspace", "msa_project", "msa_sparse_attn_bwd_workspace",
-           "msa_sparse_attn_bwd")
+           "msa_sparse_attn_bwd", "msa_qk_norm_rope", "msa_qk_norm_rope_bwd_workspace",
+           "msa_qk_norm_rope_bwd")
 
 
 def _load() -> ctypes.CDLL:
@@ -130,6 +139,13 @@ def _load() -> ctypes.CDLL:
     lib.msa_project_workspace.restype = Z
     lib.msa_project.argtypes = [PJ] + [P] * 12 + [Z, P]
     lib.msa_project.restype = I32
+    ND, F64 = ctypes.POINTER(msa_norm_rope_dims), ctypes.POINTER(ctypes.c_double)
+    lib.msa_qk_norm_rope.argtypes = [ND, F64] + [P] * 8
+    lib.msa_qk_norm_rope.restype = I32
+    lib.msa_qk_norm_rope_bwd_workspace.argtypes = [ND]
+    lib.msa_qk_norm_rope_bwd_workspace.restype = Z
+    lib.msa_qk_norm_rope_bwd.argtypes = [ND, F64] + [P] * 12 + [Z, P]
+    lib.msa_qk_norm_rope_bwd.restype = I32
     lib.msa_selftest_bounded_wait.argtypes = [P, P]
     lib.msa_selftest_bounded_wait.restype = I32
     lib.msa_profile_enable.argtypes = [ctypes.c_int32]
@@ -622,3 +638,112 @@ def quantize_fp8_rows(x: torch.Tensor, codes: Optional[torch.Tensor] = None,
                                      _stream(stream)))
     return codes, scales
 
+
+
+# ------------------------------------------------------------------ chunks of new tokens --
+# The operators below allocate (outputs, workspace) and launch on one stream of
+# the tensors' own device: `stream`, or that device's current stream.
+_NO_CONTEXT = contextlib.nullcontext()
+
+
+def _on(device: torch.device, stream):
+    """A context whose current device and stream are the call's, so that what
+    the call allocates belongs to the stream that uses it."""
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError(f"stream is on {stream.device}, the tensors are on {device}")
+        return torch.cuda.stream(stream)
+    if device.index == torch.cuda.current_device():
+        return _NO_CONTEXT
+    return torch.cuda.device(device)
+
+
+def _same_device(device: torch.device, **tensors) -> None:
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+@functools.lru_cache(maxsize=16)
+def _theta_freqs(rot_dim: int, theta: float):
+    n = rot_dim // 2
+    return (ctypes.c_double * max(n, 1))(*[theta ** (-2.0 * j / rot_dim) for j in range(n)])
+
+
+def _norm_rope_args(q, k, w_q, w_k, pos, rot_dim, theta, eps, interleaved, inv_freq):
+    if not isinstance(q, torch.Tensor) or not isinstance(k, torch.Tensor) or q.dim() != 3 \
+            or k.dim() != 3:
+        raise TypeError("q and k must be torch tensors [T, heads, d]")
+    T, H_q, d = q.shape
+    H_k = k.shape[1]
+    _want(q, "q", torch.bfloat16, (T, H_q, d))
+    _want(k, "k", torch.bfloat16, (T, H_k, d))
+    for w, name in ((w_q, "w_q"), (w_k, "w_k")):
+        if w is not None:
+            _want(w, name, torch.bfloat16, (d,))
+    _want(pos, "pos", torch.int32, (T,))
+    _same_device(q.device, k=k, w_q=w_q, w_k=w_k, pos=pos)
+    rot = d if rot_dim is None else int(rot_dim)
+    if inv_freq is not None:
+        vals = [float(f) for f in inv_freq]
+        if len(vals) != rot // 2:
+            raise ValueError(f"inv_freq must hold rot_dim / 2 = {rot // 2} values")
+        freqs = (ctypes.c_double * max(len(vals), 1))(*vals)
+    else:
+        if not theta > 0:
+            raise ValueError("theta must be positive")
+        freqs = _theta_freqs(rot, float(theta))
+    return msa_norm_rope_dims(T, H_q, H_k, d, rot, 1 if interleaved else 0, eps), freqs
+
+
+def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, w_q: Optional[torch.Tensor],
+                 w_k: Optional[torch.Tensor], pos: torch.Tensor, rot_dim: Optional[int] = None,
+                 theta: float = 10000.0, eps: float = 1e-6, interleaved: bool = False,
+                 inv_freq=None, q_out: Optional[torch.Tensor] = None,
+                 k_out: Optional[torch.Tensor] = None, stream=None
+                 ) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Per-head RMS norm (weights w_q, w_k [d] bf16, None for ones) and position
+    rotation of q [T,H_q,d] and k [T,H_k,d] bf16 at pos [T] int32: the pairs
+    (j, j + rot_dim/2), or (2j, 2j + 1) when interleaved, turn by
+    pos * inv_freq[j] (theta^(-2j/rot_dim) unless given); the rest passes
+    through.  Rows with pos < 0 are left as they were in q_out and k_out, which
+    may be q and k themselves.  Returns (q_out, k_out)."""
+    d, freqs = _norm_rope_args(q, k, w_q, w_k, pos, rot_dim, theta, eps, interleaved, inv_freq)
+    with _on(q.device, stream):
+        q_out = torch.empty_like(q) if q_out is None else q_out
+        k_out = torch.empty_like(k) if k_out is None else k_out
+        _want(q_out, "q_out", torch.bfloat16, q.shape)
+        _want(k_out, "k_out", torch.bfloat16, k.shape)
+        _same_device(q.device, q_out=q_out, k_out=k_out)
+        _raise("msa_qk_norm_rope",
+               LIB.msa_qk_norm_rope(ctypes.byref(d), freqs, _ptr(q), _ptr(k), _ptr(w_q),
+                                    _ptr(w_k), _ptr(pos), _ptr(q_out), _ptr(k_out),
+                                    _stream(stream)))
+    return q_out, k_out
+
+
+def qk_norm_rope_bwd(q: torch.Tensor, k: torch.Tensor, w_q: Optional[torch.Tensor],
+                     w_k: Optional[torch.Tensor], pos: torch.Tensor, dq_out: torch.Tensor,
+                     dk_out: torch.Tensor, rot_dim: Optional[int] = None, theta: float = 10000.0,
+                     eps: float = 1e-6, interleaved: bool = False, inv_freq=None,
+                     workspace: Optional[torch.Tensor] = None, stream=None):
+    """Backward of qk_norm_rope: (dq, dk) bf16 and (dw_q, dw_k) [d] fp32 (None
+    where the weight is None) from the forward's inputs and the gradients
+    dq_out, dk_out of its outputs.  Rows with pos < 0 get zero gradients."""
+    d, freqs = _norm_rope_args(q, k, w_q, w_k, pos, rot_dim, theta, eps, interleaved, inv_freq)
+    _want(dq_out, "dq_out", torch.bfloat16, q.shape)
+    _want(dk_out, "dk_out", torch.bfloat16, k.shape)
+    _same_device(q.device, dq_out=dq_out, dk_out=dk_out, workspace=workspace)
+    with _on(q.device, stream):
+        dq, dk = torch.empty_like(q), torch.empty_like(k)
+        dw_q, dw_k = (None if w is None else
+                      torch.empty(q.shape[2], dtype=torch.float32, device=q.device)
+                      for w in (w_q, w_k))
+        ws = _workspace(int(LIB.msa_qk_norm_rope_bwd_workspace(ctypes.byref(d))), q.device,
+                        workspace)
+        _raise("msa_qk_norm_rope_bwd",
+               LIB.msa_qk_norm_rope_bwd(ctypes.byref(d), freqs, _ptr(q), _ptr(k), _ptr(w_q),
+                                        _ptr(w_k), _ptr(pos), _ptr(dq_out), _ptr(dk_out),
+                                        _ptr(dq), _ptr(dk), _ptr(dw_q), _ptr(dw_k), _ptr(ws),
+                                        ws.numel(), _stream(stream)))
+    return dq, dk, dw_q, dw_k

@@ -11,8 +11,7 @@
 #include <string>
 #include <vector>
 
-#include "../../include/msa.h"
-#include "msa_internal.h"
+#include "capi_common.h"
 
 namespace msa {
 
@@ -102,10 +101,6 @@ void prof_end(cudaStream_t s) {
 
 namespace {
 
-constexpr size_t kStatusBytes = 256;  // status word + padding (keeps the rest 256-B aligned)
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 bool pow2_in(int x, int lo, int hi) { return x >= lo && x <= hi && (x & (x - 1)) == 0; }
 
 msa_status check_common(int64_t N, int H_q, int H_kv, int d_h, int d_idx, int B_k, int k,
@@ -162,13 +157,7 @@ namespace {
 
 thread_local cudaError_t g_last_cuda_error = cudaSuccess;
 
-msa_status from_cuda(cudaError_t e) {
-  if (e == cudaSuccess) return MSA_OK;
-  g_last_cuda_error = e;
-  return MSA_ERR_CUDA;
-}
-
-msa::DevStatus* status_of(void* ws) { return reinterpret_cast<msa::DevStatus*>(ws); }
+msa_status from_cuda(cudaError_t e) { return msa_from_cuda(e); }
 
 // Failure-detection self-test: one thread waits, through the bounded wait of
 // every kernel here, on an mbarrier that nothing completes.  The wait gives up
@@ -187,6 +176,12 @@ __global__ void selftest_wait_kernel(msa::DevStatus* st) {
 }
 
 }  // namespace
+
+msa_status msa_from_cuda(cudaError_t e) {
+  if (e == cudaSuccess) return MSA_OK;
+  g_last_cuda_error = e;
+  return MSA_ERR_CUDA;
+}
 
 extern "C" {
 

@@ -223,4 +223,26 @@ cudaError_t launch_paged_decode_fp8(const PagedLaunch& a, cudaStream_t s);
 cudaError_t launch_quantize_fp8_rows(const void* x, int64_t n_rows, int dim, void* codes,
                                      float* scales, cudaStream_t s);
 
+// Per-head RMS norm + rotation of q and k; the backward when dq_out is set.
+struct NormRopeLaunch {
+  const void* q;
+  const void* k;
+  const void* w_q;  // or null
+  const void* w_k;
+  const int32_t* pos;
+  const double* inv_freq;  // host
+  const void* dq_out;
+  const void* dk_out;
+  void* q_out;  // forward: y; backward: dx
+  void* k_out;
+  float* dw_q;
+  float* dw_k;
+  int T, H_q, H_k, d, rot;
+  bool interleaved;
+  float eps;
+  void* ws;  // backward: partial dw
+};
+size_t norm_rope_bwd_workspace_bytes(int T, int d);
+cudaError_t launch_norm_rope(const NormRopeLaunch& a, cudaStream_t s);
+
 }  // namespace msa

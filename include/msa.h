@@ -340,6 +340,44 @@ MSA_API msa_status msa_paged_decode_fp8(const msa_paged_dims* dims, const void* 
 MSA_API msa_status msa_quantize_fp8_rows(const void* x, int64_t n_rows, int32_t dim, void* codes,
                                          float* scales, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Between the projections and the attention: RMS normalisation of every query
+ * and key head, then the position rotation, in one pass.  (Not part of the
+ * method's equations, which start from Q and K; the step that a model runs on
+ * msa_project's outputs, and on q_idx and k_idx alike: H_q = H_kv, H_k = 1.)
+ *   n = x / sqrt(mean over the head of x^2 + eps),  y = R(pos) (w * n)
+ * R rotates the pairs (j, j + rot/2), or (2j, 2j + 1) when interleaved, by the
+ * angle pos * inv_freq[j], j < rot/2; dimensions rot .. d-1 pass through.
+ * Angles are exact at any int32 position (64-bit fixed point turns).
+ *   q [T, H_q, d], k [T, H_k, d] bf16      w_q, w_k [d] bf16 or NULL (ones)
+ *   pos       [T] int32; a row with pos < 0 is padding: its outputs are left
+ *             as they were, its gradients are zero and it adds nothing to dw
+ *   inv_freq  HOST array of rot/2 doubles, read during the call only (NULL
+ *             when rot = 0)
+ *   q_out, k_out: as q, k; may be q and k themselves
+ * msa_qk_norm_rope_bwd: given the gradients dq_out, dk_out of the outputs,
+ *   dq, dk bf16 (rounded once from fp32; may be dq_out and dk_out themselves)
+ *   dw_q, dw_k [d] fp32 or NULL, written: sums over all rows, in an order that
+ *   does not change from run to run.  q and k are the forward's inputs.
+ * Supported: d in {32, 64, 128}, rot a multiple of 16 up to d.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+  int32_t T, H_q, H_k, d, rot;
+  int32_t interleaved;  /* 0 or 1 */
+  float eps;            /* >= 0 */
+} msa_norm_rope_dims;
+MSA_API msa_status msa_qk_norm_rope(const msa_norm_rope_dims* dims, const double* inv_freq,
+                                    const void* q, const void* k, const void* w_q,
+                                    const void* w_k, const int32_t* pos, void* q_out, void* k_out,
+                                    void* stream);
+MSA_API size_t msa_qk_norm_rope_bwd_workspace(const msa_norm_rope_dims* dims);
+MSA_API msa_status msa_qk_norm_rope_bwd(const msa_norm_rope_dims* dims, const double* inv_freq,
+                                        const void* q, const void* k, const void* w_q,
+                                        const void* w_k, const int32_t* pos, const void* dq_out,
+                                        const void* dk_out, void* dq, void* dk, float* dw_q,
+                                        float* dw_k, void* workspace, size_t ws_bytes,
+                                        void* stream);
+
 /* Device status codes written into the workspace's status word. */
 #define MSA_DEV_OK 0
 #define MSA_DEV_TIMEOUT 1    /* a bounded on-device wait gave up; outputs invalid */
