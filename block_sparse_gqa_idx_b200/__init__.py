@@ -13,6 +13,9 @@ of ``include/msa.h``); this package is its thin Python binding:
 * ``paged_decode_fp8`` the same step on a paged FP8 (E4M3) KV cache
 * ``qk_norm_rope``    per-head RMS norm + position rotation of q and k (and
   ``qk_norm_rope_bwd``), between the projections and the attention
+* ``paged_append_fp8``, ``paged_gather_fp8``  a chunk of new tokens quantised
+  into the paged FP8 cache, and cached tokens read back (``chunk_positions``:
+  the positions of a chunk's rows)
 
 ``inputs`` holds the seeded synthetic workload generators.  The binding is
 loaded on first use of one of the names above and raises if the CUDA library
@@ -26,7 +29,8 @@ _CAPI = ("index_topk", "sparse_attn_fwd", "forward", "sparse_decode", "device_st
          "paged_decode_fp8_workspace_size", "quantize_fp8_rows", "index_topk_varlen",
          "sparse_attn_fwd_varlen", "forward_varlen", "varlen_dims", "project",
          "varlen_workspace_size", "sparse_attn_bwd",
-         "sparse_attn_bwd_workspace_size", "qk_norm_rope", "qk_norm_rope_bwd")
+         "sparse_attn_bwd_workspace_size", "qk_norm_rope", "qk_norm_rope_bwd",
+         "chunk_dims", "chunk_positions", "paged_append_fp8", "paged_gather_fp8")
 
 __all__ = list(_CAPI) + ["inputs"]
 

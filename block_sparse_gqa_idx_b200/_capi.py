@@ -66,6 +66,14 @@ class msa_norm_rope_dims(ctypes.Structure):
                 ("eps", ctypes.c_float)]
 
 
+class msa_chunk_dims(ctypes.Structure):
+    _fields_ = [("S", ctypes.c_int32), ("T", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("n_pages", ctypes.c_int64), ("H_q", ctypes.c_int32), ("H_kv", ctypes.c_int32),
+                ("d_h", ctypes.c_int32), ("d_idx", ctypes.c_int32), ("B_k", ctypes.c_int32),
+                ("k", ctypes.c_int32), ("attn_scale", ctypes.c_float),
+                ("idx_scale", ctypes.c_float)]
+
+
 class msa_kernel_time(ctypes.Structure):
     _fields_ = [("name", ctypes.c_char * 48), ("launches", ctypes.c_int32),
                 ("total_ms", ctypes.c_double)]
@@ -82,7 +90,8 @@ EXPORTS = ("msa_index_topk_workspace", "msa_index_topk", "msa_sparse_attn_fwd_wo
            "msa_sparse_attn_fwd_varlen_workspace", "msa_sparse_attn_fwd_varlen",
            "msa_project_workspace", "msa_project", "msa_sparse_attn_bwd_workspace",
            "msa_sparse_attn_bwd", "msa_qk_norm_rope", "msa_qk_norm_rope_bwd_workspace",
-           "msa_qk_norm_rope_bwd")
+           "msa_qk_norm_rope_bwd", "msa_chunk_positions", "msa_paged_append_fp8",
+           "msa_paged_gather_fp8")
 
 
 def _load() -> ctypes.CDLL:
@@ -146,6 +155,13 @@ def _load() -> ctypes.CDLL:
     lib.msa_qk_norm_rope_bwd_workspace.restype = Z
     lib.msa_qk_norm_rope_bwd.argtypes = [ND, F64] + [P] * 12 + [Z, P]
     lib.msa_qk_norm_rope_bwd.restype = I32
+    CD = ctypes.POINTER(msa_chunk_dims)
+    lib.msa_chunk_positions.argtypes = [CD] + [P] * 4
+    lib.msa_chunk_positions.restype = I32
+    lib.msa_paged_append_fp8.argtypes = [CD] + [P] * 13 + [Z, P]
+    lib.msa_paged_append_fp8.restype = I32
+    lib.msa_paged_gather_fp8.argtypes = [CD] + [P] * 13 + [Z, P]
+    lib.msa_paged_gather_fp8.restype = I32
     lib.msa_selftest_bounded_wait.argtypes = [P, P]
     lib.msa_selftest_bounded_wait.restype = I32
     lib.msa_profile_enable.argtypes = [ctypes.c_int32]
@@ -747,3 +763,144 @@ def qk_norm_rope_bwd(q: torch.Tensor, k: torch.Tensor, w_q: Optional[torch.Tenso
                                         _ptr(dq), _ptr(dk), _ptr(dw_q), _ptr(dw_k), _ptr(ws),
                                         ws.numel(), _stream(stream)))
     return dq, dk, dw_q, dw_k
+
+
+def chunk_dims(S, T, max_pages, n_pages, H_q, H_kv, d_h, d_idx, B_k, k, attn_scale=0.0,
+               idx_scale=0.0) -> msa_chunk_dims:
+    return msa_chunk_dims(int(S), int(T), int(max_pages), int(n_pages), int(H_q), int(H_kv),
+                          int(d_h), int(d_idx), int(B_k), int(k), float(attn_scale),
+                          float(idx_scale))
+
+
+def _status_ws(workspace: Optional[torch.Tensor], device):
+    """(pointer, bytes) of a workspace that holds the status word only, or none."""
+    if workspace is None:
+        return None, 0
+    _same_device(device, workspace=workspace)
+    ws = _workspace(256, device, workspace)
+    return _ptr(ws), ws.numel()
+
+
+def _want_seqs(cu_new, seq_len, page_table, device) -> Tuple[int, int]:
+    """Check the sequences' arrays; returns (S, max_pages)."""
+    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
+        raise TypeError("page_table must be a torch tensor [S, max_pages]")
+    S, max_pages = page_table.shape
+    _want(page_table, "page_table", torch.int32, (S, max_pages))
+    _want(cu_new, "cu_new", torch.int32, (S + 1,))
+    _want(seq_len, "seq_len", torch.int32, (S,))
+    _same_device(device, cu_new=cu_new, seq_len=seq_len, page_table=page_table)
+    return S, max_pages
+
+
+def _want_pages(k_pages, k_scale, v_pages, v_scale, device):
+    if not isinstance(k_pages, torch.Tensor) or k_pages.dim() != 4:
+        raise TypeError("k_pages must be a torch tensor [pages, B_k, H_kv, d_h]")
+    P, B_k, H_kv, d_h = k_pages.shape
+    _want(k_pages, "k_pages", torch.uint8, (P, B_k, H_kv, d_h))
+    _want(v_pages, "v_pages", torch.uint8, (P, B_k, H_kv, d_h))
+    _want(k_scale, "k_scale", torch.float32, (P, B_k, H_kv))
+    _want(v_scale, "v_scale", torch.float32, (P, B_k, H_kv))
+    _same_device(device, k_pages=k_pages, k_scale=k_scale, v_pages=v_pages, v_scale=v_scale)
+    return P, B_k, H_kv, d_h
+
+
+def _want_index_pages(kidx_pages, kidx_scale, device):
+    if not isinstance(kidx_pages, torch.Tensor) or kidx_pages.dim() != 3:
+        raise TypeError("kidx_pages must be a torch tensor [pages, B_k, d_idx]")
+    P, B_k, d_idx = kidx_pages.shape
+    _want(kidx_pages, "kidx_pages", torch.uint8, (P, B_k, d_idx))
+    _want(kidx_scale, "kidx_scale", torch.float32, (P, B_k))
+    _same_device(device, kidx_pages=kidx_pages, kidx_scale=kidx_scale)
+    return P, B_k, d_idx
+
+
+def chunk_positions(cu_new: torch.Tensor, seq_len: torch.Tensor, T: int, max_len: int = 2**30,
+                    pos: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Positions [T] int32 of a chunk's rows: sequence s owns rows cu_new[s] ..
+    cu_new[s+1]-1 and has seq_len[s] tokens before them ([S+1] and [S] int32,
+    device).  -1 for rows that no sequence holds, and for all rows of a
+    sequence that would grow past max_len (a multiple of 64) tokens."""
+    if not isinstance(seq_len, torch.Tensor) or seq_len.dim() != 1:
+        raise TypeError("seq_len must be a torch tensor [S]")
+    S = seq_len.shape[0]
+    _want(seq_len, "seq_len", torch.int32, (S,))
+    _want(cu_new, "cu_new", torch.int32, (S + 1,))
+    if max_len < 64 or max_len % 64 != 0:
+        raise ValueError("max_len must be a positive multiple of 64")
+    _same_device(seq_len.device, cu_new=cu_new, pos=pos)
+    d = chunk_dims(S, T, max_len // 64, 1, 1, 1, 64, 64, 64, 1)
+    with _on(seq_len.device, stream):
+        if pos is None:
+            pos = torch.empty((T,), dtype=torch.int32, device=seq_len.device)
+        _want(pos, "pos", torch.int32, (T,))
+        _raise("msa_chunk_positions",
+               LIB.msa_chunk_positions(ctypes.byref(d), _ptr(cu_new), _ptr(seq_len), _ptr(pos),
+                                       _stream(stream)))
+    return pos
+
+
+def paged_append_fp8(k_new: torch.Tensor, v_new: torch.Tensor, k_idx_new: torch.Tensor, k_pages,
+                     k_scale, v_pages, v_scale, kidx_pages, kidx_scale, page_table, cu_new,
+                     seq_len, workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Quantise a chunk of new tokens into the pages of a paged FP8 cache, by the
+    decode step's rule: k_new, v_new [T,H_kv,d_h] and k_idx_new [T,d_idx] bf16;
+    pools and page_table as paged_decode_fp8's; row t of sequence s (rows
+    cu_new[s] .. cu_new[s+1]-1) goes to position seq_len[s] + t - cu_new[s].
+    seq_len does not change.  ``workspace`` (256 bytes) only records the status
+    for device_status."""
+    device = k_pages.device
+    P, B_k, H_kv, d_h = _want_pages(k_pages, k_scale, v_pages, v_scale, device)
+    P2, B2, d_idx = _want_index_pages(kidx_pages, kidx_scale, device)
+    if (P2, B2) != (P, B_k):
+        raise ValueError(f"kidx_pages must hold {P} pages of {B_k} tokens, got {P2} of {B2}")
+    S, max_pages = _want_seqs(cu_new, seq_len, page_table, device)
+    T = k_new.shape[0]
+    _want(k_new, "k_new", torch.bfloat16, (T, H_kv, d_h))
+    _want(v_new, "v_new", torch.bfloat16, (T, H_kv, d_h))
+    _want(k_idx_new, "k_idx_new", torch.bfloat16, (T, d_idx))
+    _same_device(device, k_new=k_new, v_new=v_new, k_idx_new=k_idx_new)
+    d = chunk_dims(S, T, max_pages, P, H_kv, H_kv, d_h, d_idx, B_k, 1)
+    with _on(device, stream):
+        ws, n = _status_ws(workspace, device)
+        _raise("msa_paged_append_fp8",
+               LIB.msa_paged_append_fp8(ctypes.byref(d), _ptr(k_new), _ptr(v_new),
+                                        _ptr(k_idx_new), _ptr(k_pages), _ptr(k_scale),
+                                        _ptr(v_pages), _ptr(v_scale), _ptr(kidx_pages),
+                                        _ptr(kidx_scale), _ptr(page_table), _ptr(cu_new),
+                                        _ptr(seq_len), ws, n, _stream(stream)))
+
+
+def paged_gather_fp8(k_pages, k_scale, v_pages, v_scale, kidx_pages, kidx_scale, page_table,
+                     cu_rows, start, T: int, out=None, workspace: Optional[torch.Tensor] = None,
+                     stream=None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """Read cached tokens of a paged FP8 cache back as bf16: (k, v [T,H_kv,d_h],
+    k_idx [T,d_idx]), where row t of sequence s (rows cu_rows[s] ..
+    cu_rows[s+1]-1) is its position start[s] + t - cu_rows[s].  ``out``: the
+    three tensors to write instead of new ones."""
+    device = k_pages.device
+    P, B_k, H_kv, d_h = _want_pages(k_pages, k_scale, v_pages, v_scale, device)
+    P2, B2, d_idx = _want_index_pages(kidx_pages, kidx_scale, device)
+    if (P2, B2) != (P, B_k):
+        raise ValueError(f"kidx_pages must hold {P} pages of {B_k} tokens, got {P2} of {B2}")
+    S, max_pages = _want_seqs(cu_rows, start, page_table, device)
+    d = chunk_dims(S, T, max_pages, P, H_kv, H_kv, d_h, d_idx, B_k, 1)
+    with _on(device, stream):
+        if out is None:
+            k = torch.empty((T, H_kv, d_h), dtype=torch.bfloat16, device=device)
+            v = torch.empty((T, H_kv, d_h), dtype=torch.bfloat16, device=device)
+            k_idx = torch.empty((T, d_idx), dtype=torch.bfloat16, device=device)
+        else:
+            k, v, k_idx = out
+            _want(k, "k", torch.bfloat16, (T, H_kv, d_h))
+            _want(v, "v", torch.bfloat16, (T, H_kv, d_h))
+            _want(k_idx, "k_idx", torch.bfloat16, (T, d_idx))
+            _same_device(device, k=k, v=v, k_idx=k_idx)
+        ws, n = _status_ws(workspace, device)
+        _raise("msa_paged_gather_fp8",
+               LIB.msa_paged_gather_fp8(ctypes.byref(d), _ptr(k_pages), _ptr(k_scale),
+                                        _ptr(v_pages), _ptr(v_scale), _ptr(kidx_pages),
+                                        _ptr(kidx_scale), _ptr(page_table), _ptr(cu_rows),
+                                        _ptr(start), _ptr(k), _ptr(v), _ptr(k_idx), ws, n,
+                                        _stream(stream)))
+    return k, v, k_idx

@@ -2,8 +2,61 @@
 // of new tokens: argument validation, workspace sizing and launches.  As in
 // msa_capi.cu, nothing is allocated here.
 #include "capi_common.h"
+#include "chunk_launch.h"
 
 namespace {
+
+constexpr int64_t kInt31 = int64_t(1) << 31;
+
+// Sizes of a chunk call; need_*: which of them the call uses.
+msa_status check_chunk(const msa_chunk_dims* d, bool need_dh, bool need_didx, bool need_q) {
+  if (d == nullptr || d->S < 1 || d->T < 0 || d->max_pages < 1 || d->n_pages < 1 || d->H_kv < 1)
+    return MSA_ERR_INVALID_ARG;
+  if (!(d->attn_scale >= 0.0f) || !(d->idx_scale >= 0.0f) || isinf(d->attn_scale) ||
+      isinf(d->idx_scale))
+    return MSA_ERR_INVALID_ARG;
+  if (need_q && (d->H_q < 1 || d->H_q % d->H_kv != 0 || d->k < 1)) return MSA_ERR_INVALID_ARG;
+  if (d->B_k != 64 && d->B_k != 128) return MSA_ERR_UNSUPPORTED;
+  if (d->H_kv > 8) return MSA_ERR_UNSUPPORTED;
+  if (need_dh && d->d_h != 64 && d->d_h != 128) return MSA_ERR_UNSUPPORTED;
+  if (need_didx && d->d_idx != 64 && d->d_idx != 128) return MSA_ERR_UNSUPPORTED;
+  if (need_q && (d->H_q / d->H_kv > 16 || d->k > 32)) return MSA_ERR_UNSUPPORTED;
+  // positions, page numbers, row numbers and grids stay in 31 bits
+  if (int64_t(d->max_pages) * d->B_k >= kInt31 || d->n_pages >= kInt31)
+    return MSA_ERR_UNSUPPORTED;
+  if (int64_t(d->T) * d->H_kv * 16 >= kInt31) return MSA_ERR_UNSUPPORTED;
+  if (need_q && int64_t(d->T) * d->H_q >= kInt31) return MSA_ERR_UNSUPPORTED;
+  return MSA_OK;
+}
+
+msa::ChunkSeqs chunk_seqs(const msa_chunk_dims* d, const int32_t* cu, const int32_t* seq_len,
+                          const int32_t* table) {
+  msa::ChunkSeqs c{};
+  c.cu = cu;
+  c.seq_len = seq_len;
+  c.table = table;
+  c.S = d->S;
+  c.T = d->T;
+  c.max_pages = d->max_pages;
+  c.n_pages = d->n_pages;
+  c.B_k = d->B_k;
+  return c;
+}
+
+// A workspace that holds the status word only: absent, or cleared.
+msa_status clear_status(void* ws, size_t ws_bytes, cudaStream_t s) {
+  if (ws == nullptr) return MSA_OK;
+  if (!aligned16(ws)) return MSA_ERR_INVALID_ARG;
+  if (ws_bytes < kStatusBytes) return MSA_ERR_WORKSPACE_TOO_SMALL;
+  return msa_from_cuda(cudaMemsetAsync(ws, 0, sizeof(msa::DevStatus), s));
+}
+
+template <size_t N>
+bool all_aligned(const void* const (&ptrs)[N]) {
+  for (const void* p : ptrs)
+    if (p == nullptr || !aligned16(p)) return false;
+  return true;
+}
 
 msa_status check_norm_rope(const msa_norm_rope_dims* d, const double* inv_freq, bool need_freq) {
   if (d == nullptr || d->T < 0 || d->H_q < 1 || d->H_k < 1 || d->d < 1 || d->rot < 0 ||
@@ -104,6 +157,84 @@ msa_status msa_qk_norm_rope_bwd(const msa_norm_rope_dims* d, const double* inv_f
   a.dw_k = dw_k;
   a.ws = static_cast<uint8_t*>(ws) + kStatusBytes;
   return msa_from_cuda(msa::launch_norm_rope(a, s));
+}
+
+// ---------------------------------------------------------- paged FP8 cache --
+msa_status msa_chunk_positions(const msa_chunk_dims* d, const int32_t* cu_new,
+                               const int32_t* seq_len, int32_t* pos, void* stream) {
+  msa::NvtxRange nvtx_range("msa_chunk_positions");
+  msa_status st = check_chunk(d, false, false, false);
+  if (st != MSA_OK) return st;
+  if (d->T == 0) return MSA_OK;
+  if (!all_aligned({cu_new, seq_len, pos})) return MSA_ERR_INVALID_ARG;
+  return msa_from_cuda(msa::launch_chunk_positions(chunk_seqs(d, cu_new, seq_len, nullptr), pos,
+                                                   reinterpret_cast<cudaStream_t>(stream)));
+}
+
+msa_status msa_paged_append_fp8(const msa_chunk_dims* d, const void* k_new, const void* v_new,
+                                const void* k_idx_new, void* k_pages, float* k_scale,
+                                void* v_pages, float* v_scale, void* kidx_pages,
+                                float* kidx_scale, const int32_t* page_table,
+                                const int32_t* cu_new, const int32_t* seq_len, void* ws,
+                                size_t ws_bytes, void* stream) {
+  msa::NvtxRange nvtx_range("msa_paged_append_fp8");
+  msa_status st = check_chunk(d, true, true, false);
+  if (st != MSA_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (d->T > 0 && !all_aligned({k_new, v_new, k_idx_new, k_pages, k_scale, v_pages, v_scale,
+                                kidx_pages, kidx_scale, page_table, cu_new, seq_len}))
+    return MSA_ERR_INVALID_ARG;
+  st = clear_status(ws, ws_bytes, s);
+  if (st != MSA_OK || d->T == 0) return st;
+  msa::CacheLaunch a{};
+  a.c = chunk_seqs(d, cu_new, seq_len, page_table);
+  a.x[0] = k_new;
+  a.x[1] = v_new;
+  a.x[2] = k_idx_new;
+  a.codes[0] = k_pages;
+  a.codes[1] = v_pages;
+  a.codes[2] = kidx_pages;
+  a.scale[0] = k_scale;
+  a.scale[1] = v_scale;
+  a.scale[2] = kidx_scale;
+  a.H_kv = d->H_kv;
+  a.d_h = d->d_h;
+  a.d_idx = d->d_idx;
+  a.status = ws != nullptr ? status_of(ws) : nullptr;
+  return msa_from_cuda(msa::launch_paged_append(a, s));
+}
+
+msa_status msa_paged_gather_fp8(const msa_chunk_dims* d, const void* k_pages,
+                                const float* k_scale, const void* v_pages, const float* v_scale,
+                                const void* kidx_pages, const float* kidx_scale,
+                                const int32_t* page_table, const int32_t* cu_rows,
+                                const int32_t* start, void* k, void* v, void* k_idx, void* ws,
+                                size_t ws_bytes, void* stream) {
+  msa::NvtxRange nvtx_range("msa_paged_gather_fp8");
+  msa_status st = check_chunk(d, true, true, false);
+  if (st != MSA_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (d->T > 0 && !all_aligned({k_pages, k_scale, v_pages, v_scale, kidx_pages, kidx_scale,
+                                page_table, cu_rows, start, k, v, k_idx}))
+    return MSA_ERR_INVALID_ARG;
+  st = clear_status(ws, ws_bytes, s);
+  if (st != MSA_OK || d->T == 0) return st;
+  msa::CacheLaunch a{};
+  a.c = chunk_seqs(d, cu_rows, start, page_table);
+  a.y[0] = k;
+  a.y[1] = v;
+  a.y[2] = k_idx;
+  a.codes[0] = const_cast<void*>(k_pages);
+  a.codes[1] = const_cast<void*>(v_pages);
+  a.codes[2] = const_cast<void*>(kidx_pages);
+  a.scale[0] = const_cast<float*>(k_scale);
+  a.scale[1] = const_cast<float*>(v_scale);
+  a.scale[2] = const_cast<float*>(kidx_scale);
+  a.H_kv = d->H_kv;
+  a.d_h = d->d_h;
+  a.d_idx = d->d_idx;
+  a.status = ws != nullptr ? status_of(ws) : nullptr;
+  return msa_from_cuda(msa::launch_paged_gather(a, s));
 }
 
 }  // extern "C"

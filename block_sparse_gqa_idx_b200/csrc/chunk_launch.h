@@ -1,0 +1,21 @@
+// chunk_launch.h -- launchers of the chunk operators (chunk_capi.cu calls them).
+#pragma once
+#include "chunk_common.cuh"
+
+namespace msa {
+
+// K, V and index-key rows of the chunk's tokens and their pages.
+struct CacheLaunch {
+  ChunkSeqs c;
+  const void* x[3];  // append reads these bf16 rows
+  void* y[3];        // gather writes these
+  void* codes[3];
+  float* scale[3];
+  int H_kv, d_h, d_idx;
+  DevStatus* status;  // or null
+};
+cudaError_t launch_paged_append(const CacheLaunch& a, cudaStream_t s);
+cudaError_t launch_paged_gather(const CacheLaunch& a, cudaStream_t s);
+cudaError_t launch_chunk_positions(const ChunkSeqs& c, int32_t* pos, cudaStream_t s);
+
+}  // namespace msa

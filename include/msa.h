@@ -378,6 +378,65 @@ MSA_API msa_status msa_qk_norm_rope_bwd(const msa_norm_rope_dims* dims, const do
                                         float* dw_k, void* workspace, size_t ws_bytes,
                                         void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Chunks of new tokens on the paged FP8 cache (the pools of
+ * msa_paged_decode_fp8): chunked prefill, prefixes that are already cached,
+ * batches that mix prompts with single tokens.  One call has T rows of new
+ * tokens; sequence s owns rows cu_new[s] .. cu_new[s+1]-1 (any number, zero
+ * too) and had seq_len[s] tokens in its pages before them, so row t sits at
+ * position seq_len[s] + t - cu_new[s].
+ *   cu_new    [S+1] int32, device (so the calls can be captured into a graph):
+ *             0 = cu_new[0] <= cu_new[1] <= ... <= cu_new[S] <= T; rows from
+ *             cu_new[S] on are padding
+ *   seq_len   [S] int32, device; none of the calls below but
+ *             msa_paged_chunk_fp8 changes it
+ * Rows of padding, and all rows of a sequence whose chunk does not fit its
+ * max_pages * B_k tokens (recorded as MSA_DEV_CACHE_FULL), are skipped: their
+ * outputs are left as they were.  A page index outside [0, n_pages) is
+ * skipped and recorded as MSA_DEV_BAD_INDEX.  A workspace that the *_workspace
+ * query gives as 256 bytes holds the status word only and may be NULL (nothing
+ * is recorded then).  T = 0 is no work and MSA_OK.
+ * Supported: d_h, d_idx, B_k in {64,128}, H_kv <= 8, H_q/H_kv <= 16,
+ * 1 <= k <= 32, max_pages * B_k, n_pages, T * H_q and 16 * T * H_kv below 2^31.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+  int32_t S, T;
+  int32_t max_pages;  /* page-table entries per sequence */
+  int64_t n_pages;    /* pages in the pool */
+  int32_t H_q, H_kv, d_h, d_idx, B_k, k;
+  float attn_scale;   /* softmax scale (0 selects 1/sqrt(d_h)) */
+  float idx_scale;    /* scale of the block scores (0 selects 1/sqrt(d_idx)) */
+} msa_chunk_dims;
+
+/* pos [T] int32, written: every row's position, -1 where it is skipped. */
+MSA_API msa_status msa_chunk_positions(const msa_chunk_dims* dims, const int32_t* cu_new,
+                                       const int32_t* seq_len, int32_t* pos, void* stream);
+
+/* Quantise the chunk's rows into their pages, with msa_paged_decode_fp8's rule
+ * (scale = amax / 448 in fp32, 1 for a zero row; code = E4M3 of the fp32
+ * quotient x / scale, nearest-even, saturated).
+ *   k_new, v_new [T, H_kv, d_h] bf16, k_idx_new [T, d_idx] bf16
+ * A page that is written to belongs to one sequence. */
+MSA_API msa_status msa_paged_append_fp8(const msa_chunk_dims* dims, const void* k_new,
+                                        const void* v_new, const void* k_idx_new, void* k_pages,
+                                        float* k_scale, void* v_pages, float* v_scale,
+                                        void* kidx_pages, float* kidx_scale,
+                                        const int32_t* page_table, const int32_t* cu_new,
+                                        const int32_t* seq_len, void* workspace, size_t ws_bytes,
+                                        void* stream);
+
+/* Read cached tokens back as bf16 (code * scale, rounded once): row t is
+ * position start[s] + t - cu_rows[s] of the sequence s that holds it, with
+ * cu_rows [S+1] and start [S] as cu_new and seq_len above.
+ *   k, v [T, H_kv, d_h] bf16, k_idx [T, d_idx] bf16, written */
+MSA_API msa_status msa_paged_gather_fp8(const msa_chunk_dims* dims, const void* k_pages,
+                                        const float* k_scale, const void* v_pages,
+                                        const float* v_scale, const void* kidx_pages,
+                                        const float* kidx_scale, const int32_t* page_table,
+                                        const int32_t* cu_rows, const int32_t* start, void* k,
+                                        void* v, void* k_idx, void* workspace, size_t ws_bytes,
+                                        void* stream);
+
 /* Device status codes written into the workspace's status word. */
 #define MSA_DEV_OK 0
 #define MSA_DEV_TIMEOUT 1    /* a bounded on-device wait gave up; outputs invalid */

@@ -58,3 +58,39 @@ def test_norm_rope_rejects_pointers_and_frequencies(capi):
     assert capi.LIB.msa_qk_norm_rope_bwd(ctypes.byref(d), freqs(32), *[FAKE] * 12, ws - 1, None) == 3
     d.T = 0  # nothing to do: no pointer is needed
     assert call(ctypes.byref(d), freqs(32), *[None] * 7, None) == 0
+
+
+def chunk(capi, **kw):
+    v = dict(S=3, T=16, max_pages=8, n_pages=32, H_q=8, H_kv=2, d_h=128, d_idx=64, B_k=128, k=4)
+    v.update(kw)
+    return capi.chunk_dims(**v)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(S=0), 1), (dict(T=-1), 1), (dict(max_pages=0), 1), (dict(n_pages=0), 1), (dict(H_kv=0), 1),
+    (dict(B_k=32), 2), (dict(H_kv=9), 2), (dict(d_h=96), 2), (dict(d_idx=32), 2), (dict(attn_scale=-1.0), 1),
+    (dict(idx_scale=float("nan")), 1), (dict(max_pages=1 << 25), 2), (dict(n_pages=1 << 31), 2),
+    (dict(T=(1 << 31) - 1), 2),
+])
+def test_cache_calls_reject_sizes_on_host(capi, kw, status):
+    d = chunk(capi, **kw)
+    assert capi.LIB.msa_paged_append_fp8(ctypes.byref(d), *[FAKE] * 13, 1 << 20, None) == status
+    assert capi.LIB.msa_paged_gather_fp8(ctypes.byref(d), *[FAKE] * 13, 1 << 20, None) == status
+
+
+def test_cache_calls_reject_pointers_on_host(capi):
+    d = chunk(capi)
+    for fn in (capi.LIB.msa_paged_append_fp8, capi.LIB.msa_paged_gather_fp8):
+        for at in range(12):
+            for p in (None, ODD):
+                args = [FAKE] * 13
+                args[at] = p
+                assert fn(ctypes.byref(d), *args, 256, None) == 1
+        assert fn(ctypes.byref(d), *[FAKE] * 12, ODD, 256, None) == 1
+        assert fn(ctypes.byref(d), *[FAKE] * 13, 255, None) == 3
+        none = chunk(capi, T=0)
+        assert fn(ctypes.byref(none), *[None] * 13, 0, None) == 0
+    for at in range(3):
+        args = [FAKE] * 3
+        args[at] = None
+        assert capi.LIB.msa_chunk_positions(ctypes.byref(d), *args, None) == 1
