@@ -16,6 +16,8 @@ of ``include/msa.h``); this package is its thin Python binding:
 * ``paged_append_fp8``, ``paged_gather_fp8``  a chunk of new tokens quantised
   into the paged FP8 cache, and cached tokens read back (``chunk_positions``:
   the positions of a chunk's rows)
+* ``paged_index_scores_fp8``, ``block_topk``  the Index Branch of a chunk on
+  that cache: block scores, and the selection from them
 
 ``inputs`` holds the seeded synthetic workload generators.  The binding is
 loaded on first use of one of the names above and raises if the CUDA library
@@ -30,7 +32,8 @@ _CAPI = ("index_topk", "sparse_attn_fwd", "forward", "sparse_decode", "device_st
          "sparse_attn_fwd_varlen", "forward_varlen", "varlen_dims", "project",
          "varlen_workspace_size", "sparse_attn_bwd",
          "sparse_attn_bwd_workspace_size", "qk_norm_rope", "qk_norm_rope_bwd",
-         "chunk_dims", "chunk_positions", "paged_append_fp8", "paged_gather_fp8")
+         "chunk_dims", "chunk_positions", "paged_append_fp8", "paged_gather_fp8",
+         "paged_index_scores_fp8", "block_topk")
 
 __all__ = list(_CAPI) + ["inputs"]
 

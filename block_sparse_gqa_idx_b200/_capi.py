@@ -91,7 +91,7 @@ EXPORTS = ("msa_index_topk_workspace", "msa_index_topk", "msa_sparse_attn_fwd_wo
            "msa_project_workspace", "msa_project", "msa_sparse_attn_bwd_workspace",
            "msa_sparse_attn_bwd", "msa_qk_norm_rope", "msa_qk_norm_rope_bwd_workspace",
            "msa_qk_norm_rope_bwd", "msa_chunk_positions", "msa_paged_append_fp8",
-           "msa_paged_gather_fp8")
+           "msa_paged_gather_fp8", "msa_paged_index_scores_fp8", "msa_block_topk")
 
 
 def _load() -> ctypes.CDLL:
@@ -162,6 +162,10 @@ def _load() -> ctypes.CDLL:
     lib.msa_paged_append_fp8.restype = I32
     lib.msa_paged_gather_fp8.argtypes = [CD] + [P] * 13 + [Z, P]
     lib.msa_paged_gather_fp8.restype = I32
+    lib.msa_paged_index_scores_fp8.argtypes = [CD] + [P] * 8 + [Z, P]
+    lib.msa_paged_index_scores_fp8.restype = I32
+    lib.msa_block_topk.argtypes = [CD] + [P] * 4
+    lib.msa_block_topk.restype = I32
     lib.msa_selftest_bounded_wait.argtypes = [P, P]
     lib.msa_selftest_bounded_wait.restype = I32
     lib.msa_profile_enable.argtypes = [ctypes.c_int32]
@@ -904,3 +908,55 @@ def paged_gather_fp8(k_pages, k_scale, v_pages, v_scale, kidx_pages, kidx_scale,
                                         _ptr(start), _ptr(k), _ptr(v), _ptr(k_idx), ws, n,
                                         _stream(stream)))
     return k, v, k_idx
+
+
+def paged_index_scores_fp8(q_idx: torch.Tensor, kidx_pages, kidx_scale, page_table, cu_new, seq_len,
+                           idx_scale: float = 0.0, scores: Optional[torch.Tensor] = None,
+                           workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Eq. 6 block scores of a chunk's rows against the paged FP8 index keys:
+    q_idx [T,H_kv,d_idx] bf16 -> scores [T,H_kv,max_pages] fp32, -inf from each
+    row's own block on.  The chunk's own keys are appended first
+    (paged_append_fp8); seq_len is the cached length before the chunk."""
+    if not isinstance(q_idx, torch.Tensor) or q_idx.dim() != 3:
+        raise TypeError("q_idx must be a torch tensor [T, H_kv, d_idx]")
+    T, H_kv, _ = q_idx.shape
+    device = q_idx.device
+    P, B_k, d_idx = _want_index_pages(kidx_pages, kidx_scale, device)
+    _want(q_idx, "q_idx", torch.bfloat16, (T, H_kv, d_idx))
+    S, max_pages = _want_seqs(cu_new, seq_len, page_table, device)
+    d = chunk_dims(S, T, max_pages, P, H_kv, H_kv, 64, d_idx, B_k, 1, idx_scale=idx_scale)
+    with _on(device, stream):
+        if scores is None:
+            scores = torch.empty((T, H_kv, max_pages), dtype=torch.float32, device=device)
+        _want(scores, "scores", torch.float32, (T, H_kv, max_pages))
+        _same_device(device, scores=scores)
+        ws, n = _status_ws(workspace, device)
+        _raise("msa_paged_index_scores_fp8",
+               LIB.msa_paged_index_scores_fp8(ctypes.byref(d), _ptr(q_idx), _ptr(kidx_pages),
+                                              _ptr(kidx_scale), _ptr(page_table), _ptr(cu_new),
+                                              _ptr(seq_len), _ptr(scores), ws, n,
+                                              _stream(stream)))
+    return scores
+
+
+def block_topk(scores: torch.Tensor, pos: torch.Tensor, B_k: int, k: int,
+               idx_out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Eq. 7 from block scores [T,H_kv,blocks] fp32: each row's own block
+    (pos / B_k, pos [T] int32) and the k-1 best blocks before it, ties to the
+    lower block, -inf and NaN never chosen -> idx [T,H_kv,k] int32, ascending,
+    -1 padded.  Rows with pos < 0 are left as they were."""
+    if not isinstance(scores, torch.Tensor) or scores.dim() != 3:
+        raise TypeError("scores must be a torch tensor [T, H_kv, blocks]")
+    T, H_kv, n = scores.shape
+    _want(scores, "scores", torch.float32, (T, H_kv, n))
+    _want(pos, "pos", torch.int32, (T,))
+    _same_device(scores.device, pos=pos, idx_out=idx_out)
+    d = chunk_dims(1, T, n, 1, H_kv, H_kv, 64, 64, B_k, k)
+    with _on(scores.device, stream):
+        if idx_out is None:
+            idx_out = torch.empty((T, H_kv, k), dtype=torch.int32, device=scores.device)
+        _want(idx_out, "idx_out", torch.int32, (T, H_kv, k))
+        _raise("msa_block_topk",
+               LIB.msa_block_topk(ctypes.byref(d), _ptr(scores), _ptr(pos), _ptr(idx_out),
+                                  _stream(stream)))
+    return idx_out

@@ -237,4 +237,45 @@ msa_status msa_paged_gather_fp8(const msa_chunk_dims* d, const void* k_pages,
   return msa_from_cuda(msa::launch_paged_gather(a, s));
 }
 
+// ------------------------------------------------------ selection of a chunk --
+msa_status msa_paged_index_scores_fp8(const msa_chunk_dims* d, const void* q_idx,
+                                      const void* kidx_pages, const float* kidx_scale,
+                                      const int32_t* page_table, const int32_t* cu_new,
+                                      const int32_t* seq_len, float* scores, void* ws,
+                                      size_t ws_bytes, void* stream) {
+  msa::NvtxRange nvtx_range("msa_paged_index_scores_fp8");
+  msa_status st = check_chunk(d, false, true, false);
+  if (st != MSA_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (d->T > 0 && !all_aligned({q_idx, kidx_pages, kidx_scale, page_table, cu_new, seq_len, scores}))
+    return MSA_ERR_INVALID_ARG;
+  st = clear_status(ws, ws_bytes, s);
+  if (st != MSA_OK || d->T == 0) return st;
+  msa::ScoreLaunch a{};
+  a.c = chunk_seqs(d, cu_new, seq_len, page_table);
+  a.q_idx = q_idx;
+  a.pages = kidx_pages;
+  a.scale = kidx_scale;
+  a.out = scores;
+  a.H_kv = d->H_kv;
+  a.d_idx = d->d_idx;
+  a.idx_scale = d->idx_scale > 0.0f ? d->idx_scale : 1.0f / sqrtf(static_cast<float>(d->d_idx));
+  a.status = ws != nullptr ? status_of(ws) : nullptr;
+  return msa_from_cuda(msa::launch_chunk_scores(a, s));
+}
+
+msa_status msa_block_topk(const msa_chunk_dims* d, const float* scores, const int32_t* pos,
+                          int32_t* idx, void* stream) {
+  msa::NvtxRange nvtx_range("msa_block_topk");
+  msa_status st = check_chunk(d, false, false, false);
+  if (st != MSA_OK) return st;
+  if (d->k < 1) return MSA_ERR_INVALID_ARG;
+  if (d->k > 32) return MSA_ERR_UNSUPPORTED;
+  if (d->T == 0) return MSA_OK;
+  if (!all_aligned({scores, pos, idx})) return MSA_ERR_INVALID_ARG;
+  return msa_from_cuda(msa::launch_block_topk(scores, pos, idx, d->T, d->H_kv, d->max_pages,
+                                              d->B_k, d->k,
+                                              reinterpret_cast<cudaStream_t>(stream)));
+}
+
 }  // extern "C"

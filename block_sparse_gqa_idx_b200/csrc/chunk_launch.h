@@ -18,4 +18,20 @@ cudaError_t launch_paged_append(const CacheLaunch& a, cudaStream_t s);
 cudaError_t launch_paged_gather(const CacheLaunch& a, cudaStream_t s);
 cudaError_t launch_chunk_positions(const ChunkSeqs& c, int32_t* pos, cudaStream_t s);
 
+// Block scores of the chunk's rows against the cached index keys.
+struct ScoreLaunch {
+  ChunkSeqs c;
+  const void* q_idx;
+  const void* pages;
+  const float* scale;
+  float* out;
+  int H_kv, d_idx;
+  float idx_scale;
+  DevStatus* status;  // or null
+};
+cudaError_t launch_chunk_scores(const ScoreLaunch& a, cudaStream_t s);
+// The selection of T x H_kv rows from n block scores each.
+cudaError_t launch_block_topk(const float* scores, const int32_t* pos, int32_t* idx, int T,
+                              int H_kv, int n, int B_k, int k, cudaStream_t s);
+
 }  // namespace msa

@@ -437,6 +437,31 @@ MSA_API msa_status msa_paged_gather_fp8(const msa_chunk_dims* dims, const void* 
                                         void* v, void* k_idx, void* workspace, size_t ws_bytes,
                                         void* stream);
 
+/* Block scores of a chunk's rows (Eq. 6 with the block max-pool) against the
+ * cached index keys, which hold the chunk's own (append first):
+ *   q_idx  [T, H_kv, d_idx] bf16
+ *   scores [T, H_kv, max_pages] fp32, written: for a block b before the row's
+ *          own, idx_scale * max over its keys j of <q_idx, e4m3(code_j)> s_j
+ *          (products that are NaN do not count); -inf for its own block, which
+ *          Eq. 7 keeps without a score, for later ones, and for a block whose
+ *          page is outside the pool
+ * Dot products are exact to fp32 accumulation: bf16 queries and E4M3 codes
+ * enter the tensor cores unrounded. */
+MSA_API msa_status msa_paged_index_scores_fp8(const msa_chunk_dims* dims, const void* q_idx,
+                                              const void* kidx_pages, const float* kidx_scale,
+                                              const int32_t* page_table, const int32_t* cu_new,
+                                              const int32_t* seq_len, float* scores,
+                                              void* workspace, size_t ws_bytes, void* stream);
+
+/* Eq. 7 from block scores: the row's own block pos / B_k and the k-1 best
+ * blocks before it (ties: the lower block; -inf and NaN are never chosen).
+ *   scores [T, H_kv, max_pages] fp32     pos [T] int32, a row with pos < 0 is
+ *                                        skipped
+ *   idx    [T, H_kv, k] int32, written: ascending, -1 padded
+ * Uses dims->T, H_kv, max_pages, B_k, k. */
+MSA_API msa_status msa_block_topk(const msa_chunk_dims* dims, const float* scores,
+                                  const int32_t* pos, int32_t* idx, void* stream);
+
 /* Device status codes written into the workspace's status word. */
 #define MSA_DEV_OK 0
 #define MSA_DEV_TIMEOUT 1    /* a bounded on-device wait gave up; outputs invalid */

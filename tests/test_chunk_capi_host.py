@@ -94,3 +94,25 @@ def test_cache_calls_reject_pointers_on_host(capi):
         args = [FAKE] * 3
         args[at] = None
         assert capi.LIB.msa_chunk_positions(ctypes.byref(d), *args, None) == 1
+
+
+@pytest.mark.parametrize("kw,status", [(dict(S=0), 1), (dict(d_idx=32), 2), (dict(B_k=96), 2), (dict(H_kv=16), 2)])
+def test_index_calls_reject_on_host(capi, kw, status):
+    d = chunk(capi, **kw)
+    assert capi.LIB.msa_paged_index_scores_fp8(ctypes.byref(d), *[FAKE] * 8, 256, None) == status
+    d = chunk(capi)
+    for at in range(7):
+        for p in (None, ODD):
+            args = [FAKE] * 8
+            args[at] = p
+            assert capi.LIB.msa_paged_index_scores_fp8(ctypes.byref(d), *args, 256, None) == 1
+    assert capi.LIB.msa_paged_index_scores_fp8(ctypes.byref(d), *[FAKE] * 8, 16, None) == 3
+
+
+@pytest.mark.parametrize("kw,status", [(dict(k=0), 1), (dict(k=33), 2), (dict(B_k=1), 2), (dict(T=-1), 1)])
+def test_topk_rejects_on_host(capi, kw, status):
+    d = chunk(capi, **kw)
+    assert capi.LIB.msa_block_topk(ctypes.byref(d), FAKE, FAKE, FAKE, None) == status
+    d = chunk(capi)
+    for args in ((None, FAKE, FAKE), (FAKE, ODD, FAKE), (FAKE, FAKE, None)):
+        assert capi.LIB.msa_block_topk(ctypes.byref(d), *args, None) == 1
