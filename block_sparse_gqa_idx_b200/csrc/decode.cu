@@ -850,11 +850,15 @@ __global__ void __launch_bounds__(128) dec8_attend_kernel(const DecParams p, con
     const int64_t row = ((pg * BK + key) * p.H_kv + r) * D_H + piece * 16;
     kcs[i] = __ldg(reinterpret_cast<const uint4*>(q8.k_pages + row));
     vcs[i] = __ldg(reinterpret_cast<const uint4*>(q8.v_pages + row));
+    // what lies behind the sequence may be any bytes, NaN codes too: a masked
+    // key's weight is 0, and 0 * NaN must not reach the sum
+    if (static_cast<int64_t>(b) * BK + key > last) vcs[i] = make_uint4(0, 0, 0, 0);
   }
   float ks_reg = 0.f, vs_reg = 0.f;
   if (threadIdx.x < BK) {
     ks_reg = __ldg(q8.k_scale + (pg * BK + threadIdx.x) * p.H_kv + r);
     vs_reg = __ldg(q8.v_scale + (pg * BK + threadIdx.x) * p.H_kv + r);
+    if (static_cast<int64_t>(b) * BK + threadIdx.x > last) vs_reg = 0.f;
   }
   // 16-code pieces -> bf16 pieces of the swizzled tile
   auto widen = [&](const uint4 (&codes)[PER_T]) {
