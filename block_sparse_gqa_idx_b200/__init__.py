@@ -18,6 +18,7 @@ of ``include/msa.h``); this package is its thin Python binding:
   the positions of a chunk's rows)
 * ``paged_index_scores_fp8``, ``block_topk``  the Index Branch of a chunk on
   that cache: block scores, and the selection from them
+* ``paged_sparse_attn_fp8``  the Main Branch of a chunk on that cache
 
 ``inputs`` holds the seeded synthetic workload generators.  The binding is
 loaded on first use of one of the names above and raises if the CUDA library
@@ -33,7 +34,8 @@ _CAPI = ("index_topk", "sparse_attn_fwd", "forward", "sparse_decode", "device_st
          "varlen_workspace_size", "sparse_attn_bwd",
          "sparse_attn_bwd_workspace_size", "qk_norm_rope", "qk_norm_rope_bwd",
          "chunk_dims", "chunk_positions", "paged_append_fp8", "paged_gather_fp8",
-         "paged_index_scores_fp8", "block_topk")
+         "paged_index_scores_fp8", "block_topk", "paged_sparse_attn_fp8",
+         "paged_sparse_attn_fp8_workspace_size")
 
 __all__ = list(_CAPI) + ["inputs"]
 

@@ -91,7 +91,8 @@ EXPORTS = ("msa_index_topk_workspace", "msa_index_topk", "msa_sparse_attn_fwd_wo
            "msa_project_workspace", "msa_project", "msa_sparse_attn_bwd_workspace",
            "msa_sparse_attn_bwd", "msa_qk_norm_rope", "msa_qk_norm_rope_bwd_workspace",
            "msa_qk_norm_rope_bwd", "msa_chunk_positions", "msa_paged_append_fp8",
-           "msa_paged_gather_fp8", "msa_paged_index_scores_fp8", "msa_block_topk")
+           "msa_paged_gather_fp8", "msa_paged_index_scores_fp8", "msa_block_topk",
+           "msa_paged_sparse_attn_fp8_workspace", "msa_paged_sparse_attn_fp8")
 
 
 def _load() -> ctypes.CDLL:
@@ -166,6 +167,10 @@ def _load() -> ctypes.CDLL:
     lib.msa_paged_index_scores_fp8.restype = I32
     lib.msa_block_topk.argtypes = [CD] + [P] * 4
     lib.msa_block_topk.restype = I32
+    lib.msa_paged_sparse_attn_fp8_workspace.argtypes = [CD]
+    lib.msa_paged_sparse_attn_fp8_workspace.restype = Z
+    lib.msa_paged_sparse_attn_fp8.argtypes = [CD] + [P] * 12 + [Z, P]
+    lib.msa_paged_sparse_attn_fp8.restype = I32
     lib.msa_selftest_bounded_wait.argtypes = [P, P]
     lib.msa_selftest_bounded_wait.restype = I32
     lib.msa_profile_enable.argtypes = [ctypes.c_int32]
@@ -960,3 +965,47 @@ def block_topk(scores: torch.Tensor, pos: torch.Tensor, B_k: int, k: int,
                LIB.msa_block_topk(ctypes.byref(d), _ptr(scores), _ptr(pos), _ptr(idx_out),
                                   _stream(stream)))
     return idx_out
+
+
+def paged_sparse_attn_fp8_workspace_size(d: msa_chunk_dims) -> int:
+    return int(LIB.msa_paged_sparse_attn_fp8_workspace(ctypes.byref(d)))
+
+
+def paged_sparse_attn_fp8(q: torch.Tensor, idx: torch.Tensor, k_pages, k_scale, v_pages, v_scale,
+                          page_table, cu_new, seq_len, attn_scale: float = 0.0,
+                          o: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                          want_lse: bool = True, workspace: Optional[torch.Tensor] = None,
+                          stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Eq. 8 for a chunk's rows on the paged FP8 cache: q [T,H_q,d_h] bf16 and
+    idx [T,H_kv,k] int32 (blocks of each row's sequence) -> o [T,H_q,d_h] bf16
+    and lse [T,H_q] fp32.  The chunk's own rows are in the cache already
+    (paged_append_fp8); seq_len is the cached length before the chunk."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise TypeError("q must be a torch tensor [T, H_q, d_h]")
+    if not isinstance(idx, torch.Tensor) or idx.dim() != 3:
+        raise TypeError("idx must be a torch tensor [T, H_kv, k]")
+    T, H_q, _ = q.shape
+    kk = idx.shape[2]
+    device = q.device
+    P, B_k, H_kv, d_h = _want_pages(k_pages, k_scale, v_pages, v_scale, device)
+    _want(q, "q", torch.bfloat16, (T, H_q, d_h))
+    _want(idx, "idx", torch.int32, (T, H_kv, kk))
+    S, max_pages = _want_seqs(cu_new, seq_len, page_table, device)
+    _same_device(device, idx=idx, o=o, lse=lse, workspace=workspace)
+    d = chunk_dims(S, T, max_pages, P, H_q, H_kv, d_h, 64, B_k, kk, attn_scale=attn_scale)
+    with _on(device, stream):
+        if o is None:
+            o = torch.empty((T, H_q, d_h), dtype=torch.bfloat16, device=device)
+        _want(o, "o", torch.bfloat16, (T, H_q, d_h))
+        if lse is None and want_lse:
+            lse = torch.empty((T, H_q), dtype=torch.float32, device=device)
+        if lse is not None:
+            _want(lse, "lse", torch.float32, (T, H_q))
+        ws = _workspace(paged_sparse_attn_fp8_workspace_size(d), device, workspace)
+        _raise("msa_paged_sparse_attn_fp8",
+               LIB.msa_paged_sparse_attn_fp8(ctypes.byref(d), _ptr(q), _ptr(idx), _ptr(k_pages),
+                                             _ptr(k_scale), _ptr(v_pages), _ptr(v_scale),
+                                             _ptr(page_table), _ptr(cu_new), _ptr(seq_len),
+                                             _ptr(o), _ptr(lse), _ptr(ws), ws.numel(),
+                                             _stream(stream)))
+    return o, lse

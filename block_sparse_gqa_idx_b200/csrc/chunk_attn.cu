@@ -1,0 +1,484 @@
+// chunk_attn.cu -- Eq. 8 for a chunk of new tokens on the paged FP8 cache:
+// exact softmax attention of every row's query heads over the keys j <= pos
+// of its selected blocks.
+//
+//   S = (q e4m3(k_j)) ks_j scale,  O = sum_j softmax(S)_j vs_j e4m3(v_j)
+//
+// Query-outer kernel: one CTA per (row, group, split of the row's keys), four
+// warps that walk the row's 16-key groups independently; no shared memory and
+// no barrier until the warps' states are joined at the end.
+//   * Codes go from global memory into MMA fragments in registers, widened to
+//     f16 there (exact), so the tensor cores see the raw codes; a key's scale
+//     multiplies its scores, a value's scale its weight.
+//   * Both products are transposed so that the 16-row side of the MMA is keys
+//     (S^T = K Q^T) or dimensions (O^T = V^T P^T) and the 8-column side the
+//     group's heads: no row is padding at G = 8.  V^T pairs keys: two keys'
+//     code words are interleaved by byte permutes before widening.
+//   * P^T is S^T's accumulator layout transposed: one movmatrix per 8 keys.
+//   * A query enters as f16 times a power of two per head (exact, as in the
+//     scores kernel).
+//   * Weights are kept relative to the largest weight-times-scale so far
+//     (ref_y), apart from the softmax's own maximum (ref_x): P fits f16 for
+//     any value scales.  Both references move only when a score passes them
+//     by more than 2^10, so a step costs one vote instead of two reductions.
+//   * The loads of the next 16 keys are in flight while these are computed.
+#include <cuda_fp8.h>
+
+#include "chunk_launch.h"
+
+namespace msa {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr float kSlack = 10.f;  // log2 of how far a weight may pass its reference
+
+struct AttendParams {
+  ChunkSeqs c;
+  const __nv_bfloat16* q;  // [T, H_q, D]
+  const int32_t* idx;      // [T, H_kv, k]
+  const uint8_t* kp;       // [n_pages, B_k, H_kv, D]
+  const uint8_t* vp;
+  const float* ks;         // [n_pages, B_k, H_kv]
+  const float* vs;
+  __nv_bfloat16* o;
+  float* lse;              // or null
+  int H_q, H_kv, G, k;
+  int nsplit;
+  float scale_log2;
+  float* part_o;           // [T, H_kv, nsplit, G, D] normalised, when nsplit > 1
+  float* part_lse;         // [T, H_kv, nsplit, G] log2 of the sum
+  DevStatus* status;
+};
+
+__device__ __forceinline__ uint32_t widen2(uint32_t c2) {
+  const __half2_raw h =
+      __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(c2 & 0xFFFFu), __NV_E4M3);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+// 8x8 b16 transpose across the warp (row lane/4, columns 2 (lane%4), +1).
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+// a in the log2 domain, relative to a reference that may be -inf (no key yet).
+__device__ __forceinline__ float rel(float a, float ref) {
+  return a - (ref == -INFINITY ? 0.f : ref);
+}
+
+template <int D, int BK, int NH>
+struct Attend {
+  static constexpr int DT = D / 4;    // K codes per thread and key
+  static constexpr int NU = DT / 16;  // their 16-byte loads
+  static constexpr int VB = D / 8;    // V codes per thread and key
+  static constexpr int VW = VB / 4;   // their 4-byte words
+  static constexpr int NK = D / 16;   // MMAs along d
+  static constexpr int MT = D / 16;   // m-tiles of O^T
+
+  struct Raw {  // 16 keys
+    uint4 k[2][NU];     // keys g, g + 8
+    uint32_t v[4][VW];  // keys 2t, 2t + 1, 2t + 8, 2t + 9
+    float ks[2], vs[2]; // keys g, g + 8
+    int j0;             // position of the first key
+  };
+
+  uint32_t bq[NH][NK][2];
+  float un[NH][2];             // scale of the raw dots of heads 2t, 2t + 1 (log2 domain)
+  float o[NH][MT][4];
+  float l[NH][2], rx[NH][2], ry[NH][2];
+
+  __device__ __forceinline__ void load_q(const AttendParams& p, int64_t row, int r, int lane) {
+    const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int n = 0; n < NH; ++n) {
+      const int h = 8 * n + g;
+      const __nv_bfloat16* qr = p.q + (row * p.H_q + r * p.G + (h < p.G ? h : 0)) * D;
+      float qv[NK][4], amax = 0.f;
+#pragma unroll
+      for (int j = 0; j < NK; ++j) {
+        const uint2 raw = __ldg(reinterpret_cast<const uint2*>(qr + t * DT + 4 * j));
+        const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&raw.x));
+        const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&raw.y));
+        qv[j][0] = a.x;
+        qv[j][1] = a.y;
+        qv[j][2] = b.x;
+        qv[j][3] = b.y;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) amax = fmaxf(amax, fabsf(qv[j][e]));
+      }
+      amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
+      amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
+      const int shift = amax > 0.f ? min(13 - ilogbf(amax), 126) : 0;
+#pragma unroll
+      for (int j = 0; j < NK; ++j) {
+        bq[n][j][0] = pack_f16(ldexpf(qv[j][0], shift), ldexpf(qv[j][1], shift));
+        bq[n][j][1] = pack_f16(ldexpf(qv[j][2], shift), ldexpf(qv[j][3], shift));
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int sh = __shfl_sync(0xFFFFFFFFu, shift, (2 * t + e) * 4);
+        un[n][e] = ldexpf(p.scale_log2, -sh);
+        l[n][e] = 0.f;
+        rx[n][e] = ry[n][e] = -INFINITY;
+      }
+#pragma unroll
+      for (int i = 0; i < MT; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.f;
+    }
+  }
+
+  __device__ __forceinline__ void load(const AttendParams& p, Raw& x, int64_t pg, int b, int key0,
+                                       int r, int lane) const {
+    const int g = lane >> 2, t = lane & 3;
+    const int64_t row0 = (pg * BK + key0) * p.H_kv + r;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int64_t row = row0 + static_cast<int64_t>(g + 8 * e) * p.H_kv;
+#pragma unroll
+      for (int u = 0; u < NU; ++u)
+        x.k[e][u] = __ldg(reinterpret_cast<const uint4*>(p.kp + row * D + t * DT) + u);
+      x.ks[e] = __ldg(p.ks + row);
+      x.vs[e] = __ldg(p.vs + row);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int64_t row = row0 + static_cast<int64_t>(2 * t + (e & 1) + 8 * (e >> 1)) * p.H_kv;
+      const uint8_t* src = p.vp + row * D + g * VB;
+      if constexpr (VW == 4) {
+        const uint4 w = __ldg(reinterpret_cast<const uint4*>(src));
+        x.v[e][0] = w.x;
+        x.v[e][1] = w.y;
+        x.v[e][2] = w.z;
+        x.v[e][3] = w.w;
+      } else {
+        const uint2 w = __ldg(reinterpret_cast<const uint2*>(src));
+        x.v[e][0] = w.x;
+        x.v[e][1] = w.y;
+      }
+    }
+    x.j0 = b * BK + key0;
+  }
+
+  __device__ __forceinline__ void step(Raw& x, int pos, int lane) {
+    const int g = lane >> 2, t = lane & 3;
+    float s[NH][4];
+#pragma unroll
+    for (int n = 0; n < NH; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+#pragma unroll
+    for (int j = 0; j < NK; ++j) {
+      const uint32_t w0 = reinterpret_cast<const uint32_t*>(x.k[0])[j];
+      const uint32_t w1 = reinterpret_cast<const uint32_t*>(x.k[1])[j];
+      const uint32_t a[4] = {widen2(w0), widen2(w1), widen2(w0 >> 16), widen2(w1 >> 16)};
+#pragma unroll
+      for (int n = 0; n < NH; ++n) mma_f16_16816(s[n], a, bq[n][j][0], bq[n][j][1]);
+    }
+    const float lv[2] = {log2f(fabsf(x.vs[0])), log2f(fabsf(x.vs[1]))};
+    const bool cut = x.j0 + 15 > pos;  // warp-uniform: some of these keys come after the row
+    float y[NH][4];
+#pragma unroll
+    for (int n = 0; n < NH; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        s[n][e] *= un[n][e & 1] * x.ks[e >> 1];
+        y[n][e] = s[n][e] + lv[e >> 1];
+        if (cut && x.j0 + g + 8 * (e >> 1) > pos) s[n][e] = y[n][e] = -INFINITY;
+      }
+    if (cut) {  // a key that is not seen may hold anything, NaN codes too
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (x.j0 + 2 * t + (e & 1) + 8 * (e >> 1) > pos)
+#pragma unroll
+          for (int w = 0; w < VW; ++w) x.v[e][w] = 0u;
+    }
+    bool pass = false;
+#pragma unroll
+    for (int n = 0; n < NH; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        pass = pass || s[n][e] > rx[n][e & 1] + kSlack || y[n][e] > ry[n][e & 1] + kSlack;
+    if (__any_sync(0xFFFFFFFFu, pass)) {
+#pragma unroll
+      for (int n = 0; n < NH; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float mx = fmax3(rx[n][e], s[n][e], s[n][e + 2]);
+          float my = fmax3(ry[n][e], y[n][e], y[n][e + 2]);
+#pragma unroll
+          for (int w = 4; w < 32; w <<= 1) {
+            mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, w));
+            my = fmaxf(my, __shfl_xor_sync(0xFFFFFFFFu, my, w));
+          }
+          l[n][e] *= exp2f(rel(rx[n][e], mx));
+          const float f = exp2f(rel(ry[n][e], my));
+#pragma unroll
+          for (int i = 0; i < MT; ++i) {
+            o[n][i][e] *= f;
+            o[n][i][e + 2] *= f;
+          }
+          rx[n][e] = mx;
+          ry[n][e] = my;
+        }
+    }
+    uint32_t pb[NH][2];
+#pragma unroll
+    for (int n = 0; n < NH; ++n) {
+      float w[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        l[n][e & 1] += ex2_ftz(rel(s[n][e], rx[n][e & 1]));
+        w[e] = copysignf(ex2_ftz(rel(y[n][e], ry[n][e & 1])), x.vs[e >> 1]);
+      }
+      pb[n][0] = transpose8(pack_f16(w[0], w[1]));
+      pb[n][1] = transpose8(pack_f16(w[2], w[3]));
+    }
+#pragma unroll
+    for (int w = 0; w < VW; ++w) {
+      const uint32_t lo01 = __byte_perm(x.v[0][w], x.v[1][w], 0x5140);
+      const uint32_t lo23 = __byte_perm(x.v[2][w], x.v[3][w], 0x5140);
+      const uint32_t hi01 = __byte_perm(x.v[0][w], x.v[1][w], 0x7362);
+      const uint32_t hi23 = __byte_perm(x.v[2][w], x.v[3][w], 0x7362);
+      const uint32_t a0[4] = {widen2(lo01), widen2(lo01 >> 16), widen2(lo23), widen2(lo23 >> 16)};
+      const uint32_t a1[4] = {widen2(hi01), widen2(hi01 >> 16), widen2(hi23), widen2(hi23 >> 16)};
+#pragma unroll
+      for (int n = 0; n < NH; ++n) {
+        mma_f16_16816(o[n][2 * w], a0, pb[n][0], pb[n][1]);
+        mma_f16_16816(o[n][2 * w + 1], a1, pb[n][0], pb[n][1]);
+      }
+    }
+  }
+};
+
+template <int D, int BK, int NH>
+__global__ void __launch_bounds__(kWarps * 32) chunk_attend_kernel(const AttendParams p) {
+  using A = Attend<D, BK, NH>;
+  constexpr int HEADS = 8 * NH;
+  constexpr int GPB = BK / 16;  // 16-key groups per block
+  __shared__ float so[kWarps][HEADS][D];
+  __shared__ float sl[kWarps][HEADS], sx[kWarps][HEADS], sy[kWarps][HEADS];
+  __shared__ int2 slots[32];  // (page, block) of the row's usable slots
+  __shared__ int n_slots;
+
+  const int sp = blockIdx.x % p.nsplit;
+  const int64_t unit = blockIdx.x / p.nsplit;  // (row, group)
+  const int row = static_cast<int>(unit / p.H_kv);
+  const int r = static_cast<int>(unit - static_cast<int64_t>(row) * p.H_kv);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const ChunkTok tok = chunk_tok(p.c, row);
+  if (tok.pos < 0) {
+    if (tok.too_long && threadIdx.x == 0) report(p.status, DEV_ERR_CACHE_FULL, 130, tok.s, row);
+    return;
+  }
+  if (warp == 0) {
+    int b = lane < p.k ? __ldg(p.idx + unit * p.k + lane) : -1;
+    if (b < -1 || b >= p.c.max_pages) {
+      report(p.status, DEV_ERR_BAD_INDEX, 131, row, b);
+      b = -1;
+    }
+    int64_t pg = -1;
+    if (b >= 0 && b <= tok.pos / BK) {
+      pg = chunk_page(p.c, tok.s, b);
+      if (pg < 0) report(p.status, DEV_ERR_BAD_INDEX, 132, tok.s, b);
+    }
+    const unsigned use = __ballot_sync(0xFFFFFFFFu, pg >= 0);
+    if (pg >= 0) slots[__popc(use & ((1u << lane) - 1))] = make_int2(static_cast<int>(pg), b);
+    if (lane == 0) n_slots = __popc(use);
+  }
+  A a;
+  a.load_q(p, row, r, lane);
+  __syncthreads();
+  const int total = n_slots * GPB;
+  const int stride = p.nsplit * kWarps;
+  // the next group from i on that holds a key of this row
+  auto seek = [&](int i) {
+    while (i < total && slots[i / GPB].y * BK + (i % GPB) * 16 > tok.pos) i += stride;
+    return i;
+  };
+  auto fetch = [&](typename A::Raw& x, int i) {
+    if (i < total) a.load(p, x, slots[i / GPB].x, slots[i / GPB].y, (i % GPB) * 16, r, lane);
+  };
+  typename A::Raw x0, x1;
+  int i = seek(sp * kWarps + warp);
+  fetch(x0, i);
+  while (i < total) {
+    const int i1 = seek(i + stride);
+    fetch(x1, i1);
+    a.step(x0, tok.pos, lane);
+    if (i1 >= total) break;
+    i = seek(i1 + stride);
+    fetch(x0, i);
+    a.step(x1, tok.pos, lane);
+  }
+
+  // join the four warps' states
+  const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+  for (int n = 0; n < NH; ++n)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int h = 8 * n + 2 * t + e;
+      float l = a.l[n][e];
+#pragma unroll
+      for (int w = 4; w < 32; w <<= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, w);
+      if (g == 0) {
+        sl[warp][h] = l;
+        sx[warp][h] = a.rx[n][e];
+        sy[warp][h] = a.ry[n][e];
+      }
+#pragma unroll
+      for (int m = 0; m < A::MT; ++m)
+        *reinterpret_cast<float2*>(&so[warp][h][g * A::VB + 2 * m]) =
+            make_float2(a.o[n][m][e], a.o[n][m][e + 2]);
+    }
+  __syncthreads();
+  for (int it = threadIdx.x; it < HEADS * (D / 8); it += kWarps * 32) {
+    const int h = it / (D / 8), d = (it - h * (D / 8)) * 8;
+    if (h >= p.G) break;
+    float X = -INFINITY, Y = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      X = fmaxf(X, sx[w][h]);
+      Y = fmaxf(Y, sy[w][h]);
+    }
+    float L = 0.f, acc[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      L += sl[w][h] * exp2f(rel(sx[w][h], X));
+      const float f = exp2f(rel(sy[w][h], Y));
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[e] = fmaf(so[w][h][d + e], f, acc[e]);
+    }
+    // L is 0 only where no key was seen; a NaN goes through.  Y is -inf where
+    // every value scale is zero: O is zero then.
+    float lse2 = -INFINITY, norm = 0.f;
+    if (L != 0.f) {
+      lse2 = X + log2f(L);
+      norm = Y == -INFINITY ? L * 0.f : exp2f(Y - X) / L;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[e] *= norm;
+    if (p.nsplit == 1) {
+      const int64_t at = static_cast<int64_t>(row) * p.H_q + r * p.G + h;
+      *reinterpret_cast<uint4*>(p.o + at * D + d) =
+          make_uint4(pack_bf16(acc[0], acc[1]), pack_bf16(acc[2], acc[3]),
+                     pack_bf16(acc[4], acc[5]), pack_bf16(acc[6], acc[7]));
+      if (d == 0 && p.lse != nullptr) p.lse[at] = lse2 * 0.6931471805599453f;
+    } else {
+      const int64_t at = (unit * p.nsplit + sp) * p.G + h;
+      float4* dst = reinterpret_cast<float4*>(p.part_o + at * D + d);
+      dst[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+      dst[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+      if (d == 0) p.part_lse[at] = lse2;
+    }
+  }
+}
+
+// Join of a row's splits: one warp per (row, head), lane s weighs split s.
+template <int D>
+__global__ void __launch_bounds__(256) chunk_join_kernel(const AttendParams p) {
+  griddep_wait();
+  constexpr int PER = D / 32;
+  const int lane = threadIdx.x & 31;
+  const int64_t w = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
+  if (w >= static_cast<int64_t>(p.c.T) * p.H_q) return;
+  const int row = static_cast<int>(w / p.H_q);
+  const int head = static_cast<int>(w - static_cast<int64_t>(row) * p.H_q);
+  if (chunk_tok(p.c, row).pos < 0) return;
+  const int r = head / p.G, h = head - r * p.G;
+  const int64_t base = (static_cast<int64_t>(row) * p.H_kv + r) * p.nsplit * p.G + h;
+  const float z = lane < p.nsplit ? p.part_lse[base + static_cast<int64_t>(lane) * p.G] : -INFINITY;
+  float m = z;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+  const float wt = exp2f(rel(z, m));
+  float sum = wt;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+  float acc[PER];
+#pragma unroll
+  for (int e = 0; e < PER; ++e) acc[e] = 0.f;
+  for (int s = 0; s < p.nsplit; ++s) {
+    const float ws = __shfl_sync(0xFFFFFFFFu, wt, s);
+    const float* src = p.part_o + (base + static_cast<int64_t>(s) * p.G) * D + lane * PER;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) acc[e] = fmaf(ws, src[e], acc[e]);
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  __nv_bfloat16* dst = p.o + w * D + lane * PER;
+#pragma unroll
+  for (int e = 0; e < PER; e += 2)
+    *reinterpret_cast<__nv_bfloat162*>(dst + e) = __floats2bfloat162_rn(acc[e] * inv, acc[e + 1] * inv);
+  if (lane == 0 && p.lse != nullptr)
+    p.lse[w] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.6931471805599453f;
+}
+
+// Splits of a row's keys: enough CTAs for three per SM, at least one 16-key
+// group for every warp.
+int splits_of(int T, int H_kv, int B_k, int k) {
+  const int64_t units = static_cast<int64_t>(T) * H_kv;
+  int64_t n = (3 * static_cast<int64_t>(num_sms()) + units - 1) / units;
+  const int most = k * B_k / 16 / kWarps;
+  if (n > most) n = most;
+  return static_cast<int>(n > 32 ? 32 : n);
+}
+
+size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+
+template <int D, int BK>
+cudaError_t launch_direct(const AttendLaunch& a, cudaStream_t s) {
+  AttendParams p{};
+  p.c = a.c;
+  p.q = static_cast<const __nv_bfloat16*>(a.q);
+  p.idx = a.idx;
+  p.kp = static_cast<const uint8_t*>(a.k_pages);
+  p.vp = static_cast<const uint8_t*>(a.v_pages);
+  p.ks = a.k_scale;
+  p.vs = a.v_scale;
+  p.o = static_cast<__nv_bfloat16*>(a.o);
+  p.lse = a.lse;
+  p.H_q = a.H_q;
+  p.H_kv = a.H_kv;
+  p.G = a.H_q / a.H_kv;
+  p.k = a.k;
+  p.nsplit = splits_of(a.c.T, a.H_kv, a.c.B_k, a.k);
+  p.scale_log2 = a.scale * 1.4426950408889634f;
+  p.status = a.status;
+  const int64_t units = static_cast<int64_t>(a.c.T) * a.H_kv;
+  p.part_o = static_cast<float*>(a.ws);
+  p.part_lse = reinterpret_cast<float*>(
+      static_cast<uint8_t*>(a.ws) + align256(sizeof(float) * units * p.nsplit * p.G * D));
+  const unsigned grid = static_cast<unsigned>(units * p.nsplit);
+  prof_begin("chunk_attend", s);
+  if (p.G <= 8) chunk_attend_kernel<D, BK, 1><<<grid, kWarps * 32, 0, s>>>(p);
+  else chunk_attend_kernel<D, BK, 2><<<grid, kWarps * 32, 0, s>>>(p);
+  prof_end(s);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || p.nsplit == 1) return e;
+  const int64_t threads = static_cast<int64_t>(a.c.T) * a.H_q * 32;
+  prof_begin("chunk_join", s);
+  e = launch_pdl(chunk_join_kernel<D>, dim3(static_cast<unsigned>((threads + 255) / 256)),
+                 dim3(256), 0, s, p);
+  prof_end(s);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace
+
+size_t chunk_attend_workspace_bytes(int T, int H_q, int H_kv, int d_h, int B_k, int k) {
+  const int n = T > 0 ? splits_of(T, H_kv, B_k, k) : 1;
+  if (n == 1) return 0;
+  const size_t rows = static_cast<size_t>(T) * H_q * n;
+  return align256(sizeof(float) * rows * d_h) + align256(sizeof(float) * rows);
+}
+
+cudaError_t launch_chunk_attend(const AttendLaunch& a, cudaStream_t s) {
+  if (a.d_h == 128)
+    return a.c.B_k == 128 ? launch_direct<128, 128>(a, s) : launch_direct<128, 64>(a, s);
+  return a.c.B_k == 128 ? launch_direct<64, 128>(a, s) : launch_direct<64, 64>(a, s);
+}
+
+}  // namespace msa

@@ -278,4 +278,49 @@ msa_status msa_block_topk(const msa_chunk_dims* d, const float* scores, const in
                                               reinterpret_cast<cudaStream_t>(stream)));
 }
 
+// ------------------------------------------------------ attention of a chunk --
+size_t msa_paged_sparse_attn_fp8_workspace(const msa_chunk_dims* d) {
+  if (check_chunk(d, true, false, true) != MSA_OK) return 0;
+  return kStatusBytes +
+         msa::chunk_attend_workspace_bytes(d->T, d->H_q, d->H_kv, d->d_h, d->B_k, d->k);
+}
+
+msa_status msa_paged_sparse_attn_fp8(const msa_chunk_dims* d, const void* q, const int32_t* idx,
+                                     const void* k_pages, const float* k_scale,
+                                     const void* v_pages, const float* v_scale,
+                                     const int32_t* page_table, const int32_t* cu_new,
+                                     const int32_t* seq_len, void* o, float* lse, void* ws,
+                                     size_t ws_bytes, void* stream) {
+  msa::NvtxRange nvtx_range("msa_paged_sparse_attn_fp8");
+  msa_status st = check_chunk(d, true, false, true);
+  if (st != MSA_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (d->T == 0) return clear_status(ws, ws_bytes, s);
+  if (!all_aligned({q, idx, k_pages, k_scale, v_pages, v_scale, page_table, cu_new, seq_len, o,
+                    ws}) ||
+      !aligned16(lse))
+    return MSA_ERR_INVALID_ARG;
+  if (ws_bytes < msa_paged_sparse_attn_fp8_workspace(d)) return MSA_ERR_WORKSPACE_TOO_SMALL;
+  st = clear_status(ws, ws_bytes, s);
+  if (st != MSA_OK) return st;
+  msa::AttendLaunch a{};
+  a.c = chunk_seqs(d, cu_new, seq_len, page_table);
+  a.q = q;
+  a.idx = idx;
+  a.k_pages = k_pages;
+  a.v_pages = v_pages;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.o = o;
+  a.lse = lse;
+  a.H_q = d->H_q;
+  a.H_kv = d->H_kv;
+  a.d_h = d->d_h;
+  a.k = d->k;
+  a.scale = d->attn_scale > 0.0f ? d->attn_scale : 1.0f / sqrtf(static_cast<float>(d->d_h));
+  a.ws = static_cast<uint8_t*>(ws) + kStatusBytes;
+  a.status = status_of(ws);
+  return msa_from_cuda(msa::launch_chunk_attend(a, s));
+}
+
 }  // extern "C"

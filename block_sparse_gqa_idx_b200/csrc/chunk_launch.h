@@ -34,4 +34,23 @@ cudaError_t launch_chunk_scores(const ScoreLaunch& a, cudaStream_t s);
 cudaError_t launch_block_topk(const float* scores, const int32_t* pos, int32_t* idx, int T,
                               int H_kv, int n, int B_k, int k, cudaStream_t s);
 
+// Eq. 8 of the chunk's rows over their selected pages.
+struct AttendLaunch {
+  ChunkSeqs c;
+  const void* q;
+  const int32_t* idx;
+  const void* k_pages;
+  const void* v_pages;
+  const float* k_scale;
+  const float* v_scale;
+  void* o;
+  float* lse;  // or null
+  int H_q, H_kv, d_h, k;
+  float scale;
+  void* ws;  // chunk_attend_workspace_bytes
+  DevStatus* status;
+};
+size_t chunk_attend_workspace_bytes(int T, int H_q, int H_kv, int d_h, int B_k, int k);
+cudaError_t launch_chunk_attend(const AttendLaunch& a, cudaStream_t s);
+
 }  // namespace msa

@@ -462,6 +462,27 @@ MSA_API msa_status msa_paged_index_scores_fp8(const msa_chunk_dims* dims, const 
 MSA_API msa_status msa_block_topk(const msa_chunk_dims* dims, const float* scores,
                                   const int32_t* pos, int32_t* idx, void* stream);
 
+/* Eq. 8 for a chunk's rows: exact softmax attention of every query head over
+ * the keys j <= pos of its group's selected blocks, in the paged FP8 cache
+ * (which holds the chunk's own rows: append first).
+ *   q    [T, H_q, d_h] bf16
+ *   idx  [T, H_kv, k] int32: blocks of the row's sequence, -1 = empty slot; an
+ *        entry appears at most once per row; blocks after the row's own and
+ *        blocks whose page is outside the pool contribute nothing; an entry
+ *        outside [-1, max_pages) is ignored and recorded as MSA_DEV_BAD_INDEX
+ *   o    [T, H_q, d_h] bf16, written (rounded once from fp32)
+ *   lse  [T, H_q] fp32 natural-log LSE of the scaled logits, or NULL
+ * A row whose selection leaves no key gets o = 0 and lse = -inf.  What lies in
+ * the pages behind a row's position never reaches it, whatever its bytes. */
+MSA_API size_t msa_paged_sparse_attn_fp8_workspace(const msa_chunk_dims* dims);
+MSA_API msa_status msa_paged_sparse_attn_fp8(const msa_chunk_dims* dims, const void* q,
+                                             const int32_t* idx, const void* k_pages,
+                                             const float* k_scale, const void* v_pages,
+                                             const float* v_scale, const int32_t* page_table,
+                                             const int32_t* cu_new, const int32_t* seq_len,
+                                             void* o, float* lse, void* workspace,
+                                             size_t ws_bytes, void* stream);
+
 /* Device status codes written into the workspace's status word. */
 #define MSA_DEV_OK 0
 #define MSA_DEV_TIMEOUT 1    /* a bounded on-device wait gave up; outputs invalid */

@@ -110,3 +110,72 @@ class Cache:
 
     def pools(self, d):
         return d["kp"], d["ks"], d["vp"], d["vs"], d["ip"], d["is"]
+
+
+def refresh(c: Cache) -> None:
+    """Recompute the dense rows of the new tokens after c.rows was changed."""
+    for s in range(c.S):
+        for name in ("k", "v", "i"):
+            codes, scale = quantise(c.rows[name][c.cu[s]: c.cu[s + 1]])
+            c.dense[s, name][c.have[s]:] = e4m3(codes) * scale.double()[..., None]
+
+
+def selection(c: Cache, k: int, holes: bool = False) -> torch.Tensor:
+    """Random selections [T, H_kv, k]: the own block and earlier ones, ascending,
+    -1 padded; with `holes`, also empty rows, blocks after the row's own and
+    rows without their own block."""
+    idx = torch.full((c.T, c.H_kv, k), -1, dtype=torch.int32)
+    pos = c.positions()
+    for t in range(c.T):
+        own = int(pos[t]) // c.B_k if pos[t] >= 0 else 0
+        for h in range(c.H_kv):
+            pick = torch.randperm(own, generator=c.g)[: k - 1].tolist() + [own]
+            if holes:
+                kind = (t + h) % 5
+                if kind == 1:
+                    pick = []
+                elif kind == 2:
+                    pick = pick[:-1]
+                elif kind == 3 and own + 1 < c.max_pages and len(pick) < k:
+                    pick = pick + [own + 1]
+            pick = sorted(pick)
+            idx[t, h, : len(pick)] = torch.tensor(pick, dtype=torch.int32)
+    return idx
+
+
+def attention(c: Cache, q, idx, scale):
+    """(o, lse, tolerances of both) in float64.
+
+    Rounding of the kernels: o is rounded to bf16 once (2^-8 of it); a weight
+    times its value's scale is rounded to 11 bits, or to 2^-25 of the largest
+    one; n products are added in fp32 (a unit of the last place, 2^-23, each);
+    an error of a score enters its weight and the sum of weights."""
+    T, H_q, d = q.shape
+    G = H_q // c.H_kv
+    o = torch.zeros(T, H_q, d, dtype=torch.float64)
+    lse = torch.full((T, H_q), -float("inf"), dtype=torch.float64)
+    otol, ltol = torch.zeros_like(o), torch.zeros(T, H_q, dtype=torch.float64)
+    pos = c.positions()
+    for s in range(c.S):
+        for t in range(int(c.cu[s]), int(c.cu[s + 1])):
+            for h in range(c.H_kv):
+                j = [torch.arange(b * c.B_k, min((b + 1) * c.B_k, int(pos[t]) + 1))
+                     for b in idx[t, h].tolist() if 0 <= b <= int(pos[t]) // c.B_k]
+                j = torch.cat(j) if j else torch.zeros(0, dtype=torch.long)
+                if not len(j):
+                    continue
+                K, V = c.dense[s, "k"][j, h], c.dense[s, "v"][j, h]
+                rows = slice(h * G, (h + 1) * G)
+                x = q[t, rows].double() @ K.T * scale
+                err = (q[t, rows].double().abs() @ K.abs().T * scale * (d * 2.0**-23 + 2.0**-20)).amax(-1)
+                z = torch.logsumexp(x, -1)
+                w = torch.exp(x - z[:, None])
+                o[t, rows], lse[t, rows] = w @ V, z
+                n = len(j)
+                mag = w @ V.abs()
+                rel = 2.0**-11 + n * 2.0**-23 + 2 * err[:, None] + 2.0**-18
+                big = (w[..., None] * V.abs()[None]).amax((1, 2)) if V.numel() else 0.0
+                # the largest weight times scale, times any code, is at most 448 times that scale
+                otol[t, rows] = o[t, rows].abs() * 2.0**-8 + rel * mag + (n * 2.0**-25 * big)[:, None]
+                ltol[t, rows] = err + 2.0**-18 + z.abs() * 2.0**-21
+    return o, lse, otol, ltol

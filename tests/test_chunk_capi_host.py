@@ -116,3 +116,29 @@ def test_topk_rejects_on_host(capi, kw, status):
     d = chunk(capi)
     for args in ((None, FAKE, FAKE), (FAKE, ODD, FAKE), (FAKE, FAKE, None)):
         assert capi.LIB.msa_block_topk(ctypes.byref(d), *args, None) == 1
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(S=0), 1), (dict(H_q=0), 1), (dict(H_q=7), 1), (dict(k=0), 1), (dict(k=33), 2), (dict(H_q=34), 2),
+    (dict(d_h=32), 2), (dict(B_k=256), 2), (dict(attn_scale=float("inf")), 1), (dict(H_kv=16, H_q=16), 2),
+])
+def test_attention_rejects_sizes_on_host(capi, kw, status):
+    d = chunk(capi, **kw)
+    assert capi.LIB.msa_paged_sparse_attn_fp8_workspace(ctypes.byref(d)) == 0
+    assert capi.LIB.msa_paged_sparse_attn_fp8(ctypes.byref(d), *[FAKE] * 12, 1 << 40, None) == status
+
+
+def test_attention_rejects_pointers_on_host(capi):
+    d = chunk(capi)
+    n = capi.LIB.msa_paged_sparse_attn_fp8_workspace(ctypes.byref(d))
+    assert n >= 256
+    for at in range(12):
+        for p in (None, ODD):
+            if at == 10 and p is None:
+                continue  # lse may be absent
+            args = [FAKE] * 12
+            args[at] = p
+            assert capi.LIB.msa_paged_sparse_attn_fp8(ctypes.byref(d), *args, n, None) == 1
+    assert capi.LIB.msa_paged_sparse_attn_fp8(ctypes.byref(d), *[FAKE] * 12, n - 1, None) == 3
+    d = chunk(capi, T=0)
+    assert capi.LIB.msa_paged_sparse_attn_fp8(ctypes.byref(d), *[None] * 12, 0, None) == 0
