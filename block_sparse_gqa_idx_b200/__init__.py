@@ -19,6 +19,7 @@ of ``include/msa.h``); this package is its thin Python binding:
 * ``paged_index_scores_fp8``, ``block_topk``  the Index Branch of a chunk on
   that cache: block scores, and the selection from them
 * ``paged_sparse_attn_fp8``  the Main Branch of a chunk on that cache
+* ``paged_chunk_fp8``  the whole step for a chunk: append, selection, attention
 
 ``inputs`` holds the seeded synthetic workload generators.  The binding is
 loaded on first use of one of the names above and raises if the CUDA library
@@ -35,7 +36,7 @@ _CAPI = ("index_topk", "sparse_attn_fwd", "forward", "sparse_decode", "device_st
          "sparse_attn_bwd_workspace_size", "qk_norm_rope", "qk_norm_rope_bwd",
          "chunk_dims", "chunk_positions", "paged_append_fp8", "paged_gather_fp8",
          "paged_index_scores_fp8", "block_topk", "paged_sparse_attn_fp8",
-         "paged_sparse_attn_fp8_workspace_size")
+         "paged_sparse_attn_fp8_workspace_size", "paged_chunk_fp8", "paged_chunk_fp8_workspace_size")
 
 __all__ = list(_CAPI) + ["inputs"]
 

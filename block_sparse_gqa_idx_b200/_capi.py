@@ -92,7 +92,8 @@ EXPORTS = ("msa_index_topk_workspace", "msa_index_topk", "msa_sparse_attn_fwd_wo
            "msa_sparse_attn_bwd", "msa_qk_norm_rope", "msa_qk_norm_rope_bwd_workspace",
            "msa_qk_norm_rope_bwd", "msa_chunk_positions", "msa_paged_append_fp8",
            "msa_paged_gather_fp8", "msa_paged_index_scores_fp8", "msa_block_topk",
-           "msa_paged_sparse_attn_fp8_workspace", "msa_paged_sparse_attn_fp8")
+           "msa_paged_sparse_attn_fp8_workspace", "msa_paged_sparse_attn_fp8",
+           "msa_paged_chunk_fp8_workspace", "msa_paged_chunk_fp8")
 
 
 def _load() -> ctypes.CDLL:
@@ -171,6 +172,10 @@ def _load() -> ctypes.CDLL:
     lib.msa_paged_sparse_attn_fp8_workspace.restype = Z
     lib.msa_paged_sparse_attn_fp8.argtypes = [CD] + [P] * 12 + [Z, P]
     lib.msa_paged_sparse_attn_fp8.restype = I32
+    lib.msa_paged_chunk_fp8_workspace.argtypes = [CD]
+    lib.msa_paged_chunk_fp8_workspace.restype = Z
+    lib.msa_paged_chunk_fp8.argtypes = [CD] + [P] * 18 + [Z, P]
+    lib.msa_paged_chunk_fp8.restype = I32
     lib.msa_selftest_bounded_wait.argtypes = [P, P]
     lib.msa_selftest_bounded_wait.restype = I32
     lib.msa_profile_enable.argtypes = [ctypes.c_int32]
@@ -1009,3 +1014,58 @@ def paged_sparse_attn_fp8(q: torch.Tensor, idx: torch.Tensor, k_pages, k_scale, 
                                              _ptr(o), _ptr(lse), _ptr(ws), ws.numel(),
                                              _stream(stream)))
     return o, lse
+
+
+def paged_chunk_fp8_workspace_size(d: msa_chunk_dims) -> int:
+    return int(LIB.msa_paged_chunk_fp8_workspace(ctypes.byref(d)))
+
+
+def paged_chunk_fp8(q, q_idx, k_new, v_new, k_idx_new, k_pages, k_scale, v_pages, v_scale,
+                    kidx_pages, kidx_scale, page_table, cu_new, seq_len, kk: int,
+                    attn_scale: float = 0.0, idx_scale: float = 0.0,
+                    o: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                    want_lse: bool = True, idx_out: Optional[torch.Tensor] = None,
+                    workspace: Optional[torch.Tensor] = None, stream=None):
+    """One step for a chunk of new tokens of ragged sequences on the paged FP8
+    cache: paged_append_fp8, paged_index_scores_fp8, block_topk and
+    paged_sparse_attn_fp8 in one call, then seq_len[s] += cu_new[s+1] -
+    cu_new[s].  q [T,H_q,d_h], q_idx [T,H_kv,d_idx], k_new, v_new [T,H_kv,d_h],
+    k_idx_new [T,d_idx] bf16.  Returns (o [T,H_q,d_h] bf16, lse [T,H_q] fp32 or
+    None, idx [T,H_kv,kk] int32)."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise TypeError("q must be a torch tensor [T, H_q, d_h]")
+    T, H_q, _ = q.shape
+    device = q.device
+    P, B_k, H_kv, d_h = _want_pages(k_pages, k_scale, v_pages, v_scale, device)
+    P2, B2, d_idx = _want_index_pages(kidx_pages, kidx_scale, device)
+    if (P2, B2) != (P, B_k):
+        raise ValueError(f"kidx_pages must hold {P} pages of {B_k} tokens, got {P2} of {B2}")
+    _want(q, "q", torch.bfloat16, (T, H_q, d_h))
+    _want(q_idx, "q_idx", torch.bfloat16, (T, H_kv, d_idx))
+    _want(k_new, "k_new", torch.bfloat16, (T, H_kv, d_h))
+    _want(v_new, "v_new", torch.bfloat16, (T, H_kv, d_h))
+    _want(k_idx_new, "k_idx_new", torch.bfloat16, (T, d_idx))
+    S, max_pages = _want_seqs(cu_new, seq_len, page_table, device)
+    _same_device(device, q_idx=q_idx, k_new=k_new, v_new=v_new, k_idx_new=k_idx_new, o=o, lse=lse,
+                 idx_out=idx_out, workspace=workspace)
+    d = chunk_dims(S, T, max_pages, P, H_q, H_kv, d_h, d_idx, B_k, kk, attn_scale, idx_scale)
+    with _on(device, stream):
+        if o is None:
+            o = torch.empty((T, H_q, d_h), dtype=torch.bfloat16, device=device)
+        _want(o, "o", torch.bfloat16, (T, H_q, d_h))
+        if lse is None and want_lse:
+            lse = torch.empty((T, H_q), dtype=torch.float32, device=device)
+        if lse is not None:
+            _want(lse, "lse", torch.float32, (T, H_q))
+        if idx_out is None:
+            idx_out = torch.empty((T, H_kv, kk), dtype=torch.int32, device=device)
+        _want(idx_out, "idx_out", torch.int32, (T, H_kv, kk))
+        ws = _workspace(paged_chunk_fp8_workspace_size(d), device, workspace)
+        _raise("msa_paged_chunk_fp8",
+               LIB.msa_paged_chunk_fp8(ctypes.byref(d), _ptr(q), _ptr(q_idx), _ptr(k_new),
+                                       _ptr(v_new), _ptr(k_idx_new), _ptr(k_pages), _ptr(k_scale),
+                                       _ptr(v_pages), _ptr(v_scale), _ptr(kidx_pages),
+                                       _ptr(kidx_scale), _ptr(page_table), _ptr(cu_new),
+                                       _ptr(seq_len), _ptr(o), _ptr(lse), _ptr(idx_out), _ptr(ws),
+                                       ws.numel(), _stream(stream)))
+    return o, lse, idx_out

@@ -86,6 +86,13 @@ msa::NormRopeLaunch norm_rope_launch(const msa_norm_rope_dims* d, const double* 
   return a;
 }
 
+size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+
+size_t scores_bytes(const msa_chunk_dims* d) {
+  return align256(sizeof(float) * static_cast<size_t>(d->T) * d->H_kv * d->max_pages);
+}
+size_t pos_bytes(const msa_chunk_dims* d) { return align256(sizeof(int32_t) * d->T); }
+
 }  // namespace
 
 extern "C" {
@@ -321,6 +328,96 @@ msa_status msa_paged_sparse_attn_fp8(const msa_chunk_dims* d, const void* q, con
   a.ws = static_cast<uint8_t*>(ws) + kStatusBytes;
   a.status = status_of(ws);
   return msa_from_cuda(msa::launch_chunk_attend(a, s));
+}
+
+// ------------------------------------------------------------ the whole step --
+size_t msa_paged_chunk_fp8_workspace(const msa_chunk_dims* d) {
+  if (check_chunk(d, true, true, true) != MSA_OK) return 0;
+  return kStatusBytes + pos_bytes(d) + scores_bytes(d) +
+         msa::chunk_attend_workspace_bytes(d->T, d->H_q, d->H_kv, d->d_h, d->B_k, d->k);
+}
+
+msa_status msa_paged_chunk_fp8(const msa_chunk_dims* d, const void* q, const void* q_idx,
+                               const void* k_new, const void* v_new, const void* k_idx_new,
+                               void* k_pages, float* k_scale, void* v_pages, float* v_scale,
+                               void* kidx_pages, float* kidx_scale, const int32_t* page_table,
+                               const int32_t* cu_new, int32_t* seq_len, void* o, float* lse,
+                               int32_t* idx_out, void* ws, size_t ws_bytes, void* stream) {
+  msa::NvtxRange nvtx_range("msa_paged_chunk_fp8");
+  msa_status st = check_chunk(d, true, true, true);
+  if (st != MSA_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (d->T == 0) return clear_status(ws, ws_bytes, s);
+  if (!all_aligned({q, q_idx, k_new, v_new, k_idx_new, k_pages, k_scale, v_pages, v_scale,
+                    kidx_pages, kidx_scale, page_table, cu_new, seq_len, o, idx_out, ws}) ||
+      !aligned16(lse))
+    return MSA_ERR_INVALID_ARG;
+  if (ws_bytes < msa_paged_chunk_fp8_workspace(d)) return MSA_ERR_WORKSPACE_TOO_SMALL;
+  st = clear_status(ws, ws_bytes, s);
+  if (st != MSA_OK) return st;
+  uint8_t* at = static_cast<uint8_t*>(ws) + kStatusBytes;
+  int32_t* pos = reinterpret_cast<int32_t*>(at);
+  at += pos_bytes(d);
+  float* scores = reinterpret_cast<float*>(at);
+  at += scores_bytes(d);
+  const msa::ChunkSeqs c = chunk_seqs(d, cu_new, seq_len, page_table);
+
+  msa::CacheLaunch ca{};
+  ca.c = c;
+  ca.x[0] = k_new;
+  ca.x[1] = v_new;
+  ca.x[2] = k_idx_new;
+  ca.codes[0] = k_pages;
+  ca.codes[1] = v_pages;
+  ca.codes[2] = kidx_pages;
+  ca.scale[0] = k_scale;
+  ca.scale[1] = v_scale;
+  ca.scale[2] = kidx_scale;
+  ca.H_kv = d->H_kv;
+  ca.d_h = d->d_h;
+  ca.d_idx = d->d_idx;
+  ca.status = status_of(ws);
+  st = msa_from_cuda(msa::launch_paged_append(ca, s));
+  if (st != MSA_OK) return st;
+  st = msa_from_cuda(msa::launch_chunk_positions(c, pos, s));
+  if (st != MSA_OK) return st;
+
+  msa::ScoreLaunch sa{};
+  sa.c = c;
+  sa.q_idx = q_idx;
+  sa.pages = kidx_pages;
+  sa.scale = kidx_scale;
+  sa.out = scores;
+  sa.H_kv = d->H_kv;
+  sa.d_idx = d->d_idx;
+  sa.idx_scale = d->idx_scale > 0.0f ? d->idx_scale : 1.0f / sqrtf(static_cast<float>(d->d_idx));
+  sa.status = status_of(ws);
+  st = msa_from_cuda(msa::launch_chunk_scores(sa, s));
+  if (st != MSA_OK) return st;
+  st = msa_from_cuda(msa::launch_block_topk(scores, pos, idx_out, d->T, d->H_kv, d->max_pages,
+                                            d->B_k, d->k, s));
+  if (st != MSA_OK) return st;
+
+  msa::AttendLaunch aa{};
+  aa.c = c;
+  aa.q = q;
+  aa.idx = idx_out;
+  aa.k_pages = k_pages;
+  aa.v_pages = v_pages;
+  aa.k_scale = k_scale;
+  aa.v_scale = v_scale;
+  aa.o = o;
+  aa.lse = lse;
+  aa.H_q = d->H_q;
+  aa.H_kv = d->H_kv;
+  aa.d_h = d->d_h;
+  aa.k = d->k;
+  aa.scale = d->attn_scale > 0.0f ? d->attn_scale : 1.0f / sqrtf(static_cast<float>(d->d_h));
+  aa.ws = at;
+  aa.status = status_of(ws);
+  st = msa_from_cuda(msa::launch_chunk_attend(aa, s));
+  if (st != MSA_OK) return st;
+  return msa_from_cuda(msa::launch_chunk_advance(c, seq_len, s));
 }
 
 }  // extern "C"

@@ -17,6 +17,7 @@ struct CacheLaunch {
 cudaError_t launch_paged_append(const CacheLaunch& a, cudaStream_t s);
 cudaError_t launch_paged_gather(const CacheLaunch& a, cudaStream_t s);
 cudaError_t launch_chunk_positions(const ChunkSeqs& c, int32_t* pos, cudaStream_t s);
+cudaError_t launch_chunk_advance(const ChunkSeqs& c, int32_t* seq_len, cudaStream_t s);
 
 // Block scores of the chunk's rows against the cached index keys.
 struct ScoreLaunch {

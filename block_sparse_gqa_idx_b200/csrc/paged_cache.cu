@@ -128,6 +128,17 @@ __global__ void __launch_bounds__(kThreads) chunk_positions_kernel(const ChunkSe
   if (t < c.T) pos[t] = chunk_tok(c, t).pos;
 }
 
+// seq_len[s] += the chunk's rows of s, where they fit (and were served).
+__global__ void __launch_bounds__(kThreads) chunk_advance_kernel(const ChunkSeqs c, int32_t* seq_len) {
+  const int s = blockIdx.x * kThreads + threadIdx.x;
+  if (s >= c.S) return;
+  const int c0 = c.cu[s], c1 = c.cu[s + 1];
+  const int len = seq_len[s];
+  if (c0 < 0 || c1 <= c0 || c1 > c.T || len < 0) return;
+  if (static_cast<int64_t>(len) + (c1 - c0) <= static_cast<int64_t>(c.max_pages) * c.B_k)
+    seq_len[s] = len + (c1 - c0);
+}
+
 CacheParams params_of(const CacheLaunch& a) {
   CacheParams p{};
   p.c = a.c;
@@ -172,6 +183,13 @@ cudaError_t launch_paged_gather(const CacheLaunch& a, cudaStream_t s) {
 cudaError_t launch_chunk_positions(const ChunkSeqs& c, int32_t* pos, cudaStream_t s) {
   prof_begin("chunk_positions", s);
   chunk_positions_kernel<<<(c.T + kThreads - 1) / kThreads, kThreads, 0, s>>>(c, pos);
+  prof_end(s);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_chunk_advance(const ChunkSeqs& c, int32_t* seq_len, cudaStream_t s) {
+  prof_begin("chunk_advance", s);
+  chunk_advance_kernel<<<(c.S + kThreads - 1) / kThreads, kThreads, 0, s>>>(c, seq_len);
   prof_end(s);
   return cudaGetLastError();
 }

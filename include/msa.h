@@ -483,6 +483,22 @@ MSA_API msa_status msa_paged_sparse_attn_fp8(const msa_chunk_dims* dims, const v
                                              void* o, float* lse, void* workspace,
                                              size_t ws_bytes, void* stream);
 
+/* The whole step for a chunk: append, block scores, Top-k, attention over the
+ * selection, and then seq_len[s] += cu_new[s+1] - cu_new[s] for every sequence
+ * that fits its pages.  Arguments as above.
+ *   idx_out [T, H_kv, k] int32: the selection used (required: the later steps
+ *           read it)
+ * The workspace also holds the scores, T * H_kv * max_pages floats. */
+MSA_API size_t msa_paged_chunk_fp8_workspace(const msa_chunk_dims* dims);
+MSA_API msa_status msa_paged_chunk_fp8(const msa_chunk_dims* dims, const void* q,
+                                       const void* q_idx, const void* k_new, const void* v_new,
+                                       const void* k_idx_new, void* k_pages, float* k_scale,
+                                       void* v_pages, float* v_scale, void* kidx_pages,
+                                       float* kidx_scale, const int32_t* page_table,
+                                       const int32_t* cu_new, int32_t* seq_len, void* o,
+                                       float* lse, int32_t* idx_out, void* workspace,
+                                       size_t ws_bytes, void* stream);
+
 /* Device status codes written into the workspace's status word. */
 #define MSA_DEV_OK 0
 #define MSA_DEV_TIMEOUT 1    /* a bounded on-device wait gave up; outputs invalid */

@@ -142,3 +142,22 @@ def test_attention_rejects_pointers_on_host(capi):
     assert capi.LIB.msa_paged_sparse_attn_fp8(ctypes.byref(d), *[FAKE] * 12, n - 1, None) == 3
     d = chunk(capi, T=0)
     assert capi.LIB.msa_paged_sparse_attn_fp8(ctypes.byref(d), *[None] * 12, 0, None) == 0
+
+
+def test_step_rejects_on_host(capi):
+    call, size = capi.LIB.msa_paged_chunk_fp8, capi.LIB.msa_paged_chunk_fp8_workspace
+    for kw, status in ((dict(S=0), 1), (dict(d_idx=32), 2), (dict(d_h=96), 2), (dict(k=40), 2), (dict(H_q=3), 1)):
+        d = chunk(capi, **kw)
+        assert size(ctypes.byref(d)) == 0
+        assert call(ctypes.byref(d), *[FAKE] * 18, 1 << 40, None) == status
+    d = chunk(capi)
+    n = size(ctypes.byref(d))
+    assert n >= 256 + 4 * 16 + 4 * 16 * 2 * 8
+    for at in range(18):
+        for p in (None, ODD):
+            if at == 15 and p is None:
+                continue  # lse may be absent
+            args = [FAKE] * 18
+            args[at] = p
+            assert call(ctypes.byref(d), *args, n, None) == 1
+    assert call(ctypes.byref(d), *[FAKE] * 18, n - 1, None) == 3
