@@ -672,8 +672,15 @@ def quantize_fp8_rows(x: torch.Tensor, codes: Optional[torch.Tensor] = None,
 
 # ------------------------------------------------------------------ chunks of new tokens --
 # The operators below allocate (outputs, workspace) and launch on one stream of
-# the tensors' own device: `stream`, or that device's current stream.
+# the tensors' own device: `stream`, or that device's current stream.  They
+# serve single tokens, where the host's share of a call counts: a tensor is
+# checked by one expression (_want spells out what is wrong with it), pointers
+# go to ctypes as integers, and what follows from sizes alone is kept.
 _NO_CONTEXT = contextlib.nullcontext()
+_BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+_Tensor = torch.Tensor
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _on(device: torch.device, stream):
@@ -688,10 +695,39 @@ def _on(device: torch.device, stream):
     return torch.cuda.device(device)
 
 
-def _same_device(device: torch.device, **tensors) -> None:
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
+def _device_of(t, name: str, ndim: int) -> torch.device:
+    """The device of the tensor that the others are checked against."""
+    if not isinstance(t, _Tensor) or t.dim() != ndim:
+        raise TypeError(f"{name} must be a torch tensor of {ndim} dimensions")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.device
+
+
+def _check(device: torch.device, *specs) -> None:
+    """Each spec (tensor, name, dtype, shape): a contiguous tensor of that type
+    and shape on `device`."""
+    for t, name, dtype, shape in specs:
+        if not (isinstance(t, _Tensor) and t.dtype is dtype and t.shape == shape
+                and t.device == device and t.is_contiguous()):
+            _want(t, name, dtype, shape)
             raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def _scratch(nbytes: int, device: torch.device, ws: Optional[torch.Tensor]) -> torch.Tensor:
+    if ws is None:
+        return torch.empty(nbytes, dtype=_U8, device=device)
+    if ws.device != device:
+        raise ValueError(f"workspace is on {ws.device}, expected {device}")
+    return _workspace(nbytes, device, ws)
+
+
+def _status_ws(ws: Optional[torch.Tensor], device: torch.device):
+    """(pointer, bytes) of a workspace that holds the status word only, or none."""
+    if ws is None:
+        return None, 0
+    ws = _scratch(256, device, ws)
+    return ws.data_ptr(), ws.numel()
 
 
 @functools.lru_cache(maxsize=16)
@@ -700,19 +736,28 @@ def _theta_freqs(rot_dim: int, theta: float):
     return (ctypes.c_double * max(n, 1))(*[theta ** (-2.0 * j / rot_dim) for j in range(n)])
 
 
+@functools.lru_cache(maxsize=256)
+def _norm_rope_dims(*sizes):
+    d = msa_norm_rope_dims(*sizes)
+    return d, ctypes.byref(d)
+
+
+@functools.lru_cache(maxsize=256)
+def _norm_rope_bwd_bytes(device_index: int, *sizes) -> int:
+    return int(LIB.msa_qk_norm_rope_bwd_workspace(_norm_rope_dims(*sizes)[1]))
+
+
 def _norm_rope_args(q, k, w_q, w_k, pos, rot_dim, theta, eps, interleaved, inv_freq):
-    if not isinstance(q, torch.Tensor) or not isinstance(k, torch.Tensor) or q.dim() != 3 \
-            or k.dim() != 3:
-        raise TypeError("q and k must be torch tensors [T, heads, d]")
+    device = _device_of(q, "q", 3)
+    _device_of(k, "k", 3)
     T, H_q, d = q.shape
     H_k = k.shape[1]
-    _want(q, "q", torch.bfloat16, (T, H_q, d))
-    _want(k, "k", torch.bfloat16, (T, H_k, d))
-    for w, name in ((w_q, "w_q"), (w_k, "w_k")):
-        if w is not None:
-            _want(w, name, torch.bfloat16, (d,))
-    _want(pos, "pos", torch.int32, (T,))
-    _same_device(q.device, k=k, w_q=w_q, w_k=w_k, pos=pos)
+    _check(device, (q, "q", _BF16, (T, H_q, d)), (k, "k", _BF16, (T, H_k, d)),
+           (pos, "pos", _I32, (T,)))
+    if w_q is not None:
+        _check(device, (w_q, "w_q", _BF16, (d,)))
+    if w_k is not None:
+        _check(device, (w_k, "w_k", _BF16, (d,)))
     rot = d if rot_dim is None else int(rot_dim)
     if inv_freq is not None:
         vals = [float(f) for f in inv_freq]
@@ -723,7 +768,7 @@ def _norm_rope_args(q, k, w_q, w_k, pos, rot_dim, theta, eps, interleaved, inv_f
         if not theta > 0:
             raise ValueError("theta must be positive")
         freqs = _theta_freqs(rot, float(theta))
-    return msa_norm_rope_dims(T, H_q, H_k, d, rot, 1 if interleaved else 0, eps), freqs
+    return device, (T, H_q, H_k, d, rot, 1 if interleaved else 0, float(eps)), freqs
 
 
 def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, w_q: Optional[torch.Tensor],
@@ -738,17 +783,23 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, w_q: Optional[torch.Tensor],
     pos * inv_freq[j] (theta^(-2j/rot_dim) unless given); the rest passes
     through.  Rows with pos < 0 are left as they were in q_out and k_out, which
     may be q and k themselves.  Returns (q_out, k_out)."""
-    d, freqs = _norm_rope_args(q, k, w_q, w_k, pos, rot_dim, theta, eps, interleaved, inv_freq)
-    with _on(q.device, stream):
-        q_out = torch.empty_like(q) if q_out is None else q_out
-        k_out = torch.empty_like(k) if k_out is None else k_out
-        _want(q_out, "q_out", torch.bfloat16, q.shape)
-        _want(k_out, "k_out", torch.bfloat16, k.shape)
-        _same_device(q.device, q_out=q_out, k_out=k_out)
+    device, sizes, freqs = _norm_rope_args(q, k, w_q, w_k, pos, rot_dim, theta, eps, interleaved,
+                                           inv_freq)
+    with _on(device, stream):
+        if q_out is None:
+            q_out = torch.empty_like(q)
+        else:
+            _check(device, (q_out, "q_out", _BF16, q.shape))
+        if k_out is None:
+            k_out = torch.empty_like(k)
+        else:
+            _check(device, (k_out, "k_out", _BF16, k.shape))
         _raise("msa_qk_norm_rope",
-               LIB.msa_qk_norm_rope(ctypes.byref(d), freqs, _ptr(q), _ptr(k), _ptr(w_q),
-                                    _ptr(w_k), _ptr(pos), _ptr(q_out), _ptr(k_out),
-                                    _stream(stream)))
+               LIB.msa_qk_norm_rope(_norm_rope_dims(*sizes)[1], freqs, q.data_ptr(), k.data_ptr(),
+                                    None if w_q is None else w_q.data_ptr(),
+                                    None if w_k is None else w_k.data_ptr(), pos.data_ptr(),
+                                    q_out.data_ptr(), k_out.data_ptr(),
+                                    _raw_stream(device.index)))
     return q_out, k_out
 
 
@@ -760,22 +811,22 @@ def qk_norm_rope_bwd(q: torch.Tensor, k: torch.Tensor, w_q: Optional[torch.Tenso
     """Backward of qk_norm_rope: (dq, dk) bf16 and (dw_q, dw_k) [d] fp32 (None
     where the weight is None) from the forward's inputs and the gradients
     dq_out, dk_out of its outputs.  Rows with pos < 0 get zero gradients."""
-    d, freqs = _norm_rope_args(q, k, w_q, w_k, pos, rot_dim, theta, eps, interleaved, inv_freq)
-    _want(dq_out, "dq_out", torch.bfloat16, q.shape)
-    _want(dk_out, "dk_out", torch.bfloat16, k.shape)
-    _same_device(q.device, dq_out=dq_out, dk_out=dk_out, workspace=workspace)
-    with _on(q.device, stream):
+    device, sizes, freqs = _norm_rope_args(q, k, w_q, w_k, pos, rot_dim, theta, eps, interleaved,
+                                           inv_freq)
+    _check(device, (dq_out, "dq_out", _BF16, q.shape), (dk_out, "dk_out", _BF16, k.shape))
+    with _on(device, stream):
         dq, dk = torch.empty_like(q), torch.empty_like(k)
-        dw_q, dw_k = (None if w is None else
-                      torch.empty(q.shape[2], dtype=torch.float32, device=q.device)
+        dw_q, dw_k = (None if w is None else torch.empty(q.shape[2], dtype=_F32, device=device)
                       for w in (w_q, w_k))
-        ws = _workspace(int(LIB.msa_qk_norm_rope_bwd_workspace(ctypes.byref(d))), q.device,
-                        workspace)
+        ws = _scratch(_norm_rope_bwd_bytes(device.index, *sizes), device, workspace)
         _raise("msa_qk_norm_rope_bwd",
-               LIB.msa_qk_norm_rope_bwd(ctypes.byref(d), freqs, _ptr(q), _ptr(k), _ptr(w_q),
-                                        _ptr(w_k), _ptr(pos), _ptr(dq_out), _ptr(dk_out),
-                                        _ptr(dq), _ptr(dk), _ptr(dw_q), _ptr(dw_k), _ptr(ws),
-                                        ws.numel(), _stream(stream)))
+               LIB.msa_qk_norm_rope_bwd(_norm_rope_dims(*sizes)[1], freqs, q.data_ptr(),
+                                        k.data_ptr(), None if w_q is None else w_q.data_ptr(),
+                                        None if w_k is None else w_k.data_ptr(), pos.data_ptr(),
+                                        dq_out.data_ptr(), dk_out.data_ptr(), dq.data_ptr(),
+                                        dk.data_ptr(), None if dw_q is None else dw_q.data_ptr(),
+                                        None if dw_k is None else dw_k.data_ptr(), ws.data_ptr(),
+                                        ws.numel(), _raw_stream(device.index)))
     return dq, dk, dw_q, dw_k
 
 
@@ -786,47 +837,43 @@ def chunk_dims(S, T, max_pages, n_pages, H_q, H_kv, d_h, d_idx, B_k, k, attn_sca
                           float(idx_scale))
 
 
-def _status_ws(workspace: Optional[torch.Tensor], device):
-    """(pointer, bytes) of a workspace that holds the status word only, or none."""
-    if workspace is None:
-        return None, 0
-    _same_device(device, workspace=workspace)
-    ws = _workspace(256, device, workspace)
-    return _ptr(ws), ws.numel()
+@functools.lru_cache(maxsize=1024)
+def _chunk_ref(*sizes):
+    return ctypes.byref(chunk_dims(*sizes))
 
 
 def _want_seqs(cu_new, seq_len, page_table, device) -> Tuple[int, int]:
     """Check the sequences' arrays; returns (S, max_pages)."""
-    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
+    if not isinstance(page_table, _Tensor) or page_table.dim() != 2:
         raise TypeError("page_table must be a torch tensor [S, max_pages]")
     S, max_pages = page_table.shape
-    _want(page_table, "page_table", torch.int32, (S, max_pages))
-    _want(cu_new, "cu_new", torch.int32, (S + 1,))
-    _want(seq_len, "seq_len", torch.int32, (S,))
-    _same_device(device, cu_new=cu_new, seq_len=seq_len, page_table=page_table)
+    _check(device, (page_table, "page_table", _I32, (S, max_pages)),
+           (cu_new, "cu_new", _I32, (S + 1,)), (seq_len, "seq_len", _I32, (S,)))
     return S, max_pages
 
 
 def _want_pages(k_pages, k_scale, v_pages, v_scale, device):
-    if not isinstance(k_pages, torch.Tensor) or k_pages.dim() != 4:
-        raise TypeError("k_pages must be a torch tensor [pages, B_k, H_kv, d_h]")
-    P, B_k, H_kv, d_h = k_pages.shape
-    _want(k_pages, "k_pages", torch.uint8, (P, B_k, H_kv, d_h))
-    _want(v_pages, "v_pages", torch.uint8, (P, B_k, H_kv, d_h))
-    _want(k_scale, "k_scale", torch.float32, (P, B_k, H_kv))
-    _want(v_scale, "v_scale", torch.float32, (P, B_k, H_kv))
-    _same_device(device, k_pages=k_pages, k_scale=k_scale, v_pages=v_pages, v_scale=v_scale)
+    _device_of(k_pages, "k_pages", 4)
+    shape = P, B_k, H_kv, d_h = k_pages.shape
+    _check(device, (k_pages, "k_pages", _U8, shape), (v_pages, "v_pages", _U8, shape),
+           (k_scale, "k_scale", _F32, shape[:3]), (v_scale, "v_scale", _F32, shape[:3]))
     return P, B_k, H_kv, d_h
 
 
 def _want_index_pages(kidx_pages, kidx_scale, device):
-    if not isinstance(kidx_pages, torch.Tensor) or kidx_pages.dim() != 3:
-        raise TypeError("kidx_pages must be a torch tensor [pages, B_k, d_idx]")
-    P, B_k, d_idx = kidx_pages.shape
-    _want(kidx_pages, "kidx_pages", torch.uint8, (P, B_k, d_idx))
-    _want(kidx_scale, "kidx_scale", torch.float32, (P, B_k))
-    _same_device(device, kidx_pages=kidx_pages, kidx_scale=kidx_scale)
+    _device_of(kidx_pages, "kidx_pages", 3)
+    shape = P, B_k, d_idx = kidx_pages.shape
+    _check(device, (kidx_pages, "kidx_pages", _U8, shape),
+           (kidx_scale, "kidx_scale", _F32, shape[:2]))
     return P, B_k, d_idx
+
+
+def _want_pools(k_pages, k_scale, v_pages, v_scale, kidx_pages, kidx_scale, device):
+    P, B_k, H_kv, d_h = _want_pages(k_pages, k_scale, v_pages, v_scale, device)
+    P2, B2, d_idx = _want_index_pages(kidx_pages, kidx_scale, device)
+    if P2 != P or B2 != B_k:
+        raise ValueError(f"kidx_pages must hold {P} pages of {B_k} tokens, got {P2} of {B2}")
+    return P, B_k, H_kv, d_h, d_idx
 
 
 def chunk_positions(cu_new: torch.Tensor, seq_len: torch.Tensor, T: int, max_len: int = 2**30,
@@ -835,22 +882,20 @@ def chunk_positions(cu_new: torch.Tensor, seq_len: torch.Tensor, T: int, max_len
     cu_new[s+1]-1 and has seq_len[s] tokens before them ([S+1] and [S] int32,
     device).  -1 for rows that no sequence holds, and for all rows of a
     sequence that would grow past max_len (a multiple of 64) tokens."""
-    if not isinstance(seq_len, torch.Tensor) or seq_len.dim() != 1:
-        raise TypeError("seq_len must be a torch tensor [S]")
+    device = _device_of(seq_len, "seq_len", 1)
     S = seq_len.shape[0]
-    _want(seq_len, "seq_len", torch.int32, (S,))
-    _want(cu_new, "cu_new", torch.int32, (S + 1,))
+    _check(device, (seq_len, "seq_len", _I32, (S,)), (cu_new, "cu_new", _I32, (S + 1,)))
     if max_len < 64 or max_len % 64 != 0:
         raise ValueError("max_len must be a positive multiple of 64")
-    _same_device(seq_len.device, cu_new=cu_new, pos=pos)
-    d = chunk_dims(S, T, max_len // 64, 1, 1, 1, 64, 64, 64, 1)
-    with _on(seq_len.device, stream):
+    with _on(device, stream):
         if pos is None:
-            pos = torch.empty((T,), dtype=torch.int32, device=seq_len.device)
-        _want(pos, "pos", torch.int32, (T,))
+            pos = torch.empty((T,), dtype=_I32, device=device)
+        else:
+            _check(device, (pos, "pos", _I32, (T,)))
         _raise("msa_chunk_positions",
-               LIB.msa_chunk_positions(ctypes.byref(d), _ptr(cu_new), _ptr(seq_len), _ptr(pos),
-                                       _stream(stream)))
+               LIB.msa_chunk_positions(_chunk_ref(S, T, max_len // 64, 1, 1, 1, 64, 64, 64, 1),
+                                       cu_new.data_ptr(), seq_len.data_ptr(), pos.data_ptr(),
+                                       _raw_stream(device.index)))
     return pos
 
 
@@ -863,26 +908,23 @@ def paged_append_fp8(k_new: torch.Tensor, v_new: torch.Tensor, k_idx_new: torch.
     cu_new[s] .. cu_new[s+1]-1) goes to position seq_len[s] + t - cu_new[s].
     seq_len does not change.  ``workspace`` (256 bytes) only records the status
     for device_status."""
-    device = k_pages.device
-    P, B_k, H_kv, d_h = _want_pages(k_pages, k_scale, v_pages, v_scale, device)
-    P2, B2, d_idx = _want_index_pages(kidx_pages, kidx_scale, device)
-    if (P2, B2) != (P, B_k):
-        raise ValueError(f"kidx_pages must hold {P} pages of {B_k} tokens, got {P2} of {B2}")
+    device = _device_of(k_new, "k_new", 3)
+    P, B_k, H_kv, d_h, d_idx = _want_pools(k_pages, k_scale, v_pages, v_scale, kidx_pages,
+                                           kidx_scale, device)
     S, max_pages = _want_seqs(cu_new, seq_len, page_table, device)
     T = k_new.shape[0]
-    _want(k_new, "k_new", torch.bfloat16, (T, H_kv, d_h))
-    _want(v_new, "v_new", torch.bfloat16, (T, H_kv, d_h))
-    _want(k_idx_new, "k_idx_new", torch.bfloat16, (T, d_idx))
-    _same_device(device, k_new=k_new, v_new=v_new, k_idx_new=k_idx_new)
-    d = chunk_dims(S, T, max_pages, P, H_kv, H_kv, d_h, d_idx, B_k, 1)
+    _check(device, (k_new, "k_new", _BF16, (T, H_kv, d_h)), (v_new, "v_new", _BF16, (T, H_kv, d_h)),
+           (k_idx_new, "k_idx_new", _BF16, (T, d_idx)))
     with _on(device, stream):
         ws, n = _status_ws(workspace, device)
         _raise("msa_paged_append_fp8",
-               LIB.msa_paged_append_fp8(ctypes.byref(d), _ptr(k_new), _ptr(v_new),
-                                        _ptr(k_idx_new), _ptr(k_pages), _ptr(k_scale),
-                                        _ptr(v_pages), _ptr(v_scale), _ptr(kidx_pages),
-                                        _ptr(kidx_scale), _ptr(page_table), _ptr(cu_new),
-                                        _ptr(seq_len), ws, n, _stream(stream)))
+               LIB.msa_paged_append_fp8(_chunk_ref(S, T, max_pages, P, H_kv, H_kv, d_h, d_idx, B_k, 1),
+                                        k_new.data_ptr(), v_new.data_ptr(), k_idx_new.data_ptr(),
+                                        k_pages.data_ptr(), k_scale.data_ptr(), v_pages.data_ptr(),
+                                        v_scale.data_ptr(), kidx_pages.data_ptr(),
+                                        kidx_scale.data_ptr(), page_table.data_ptr(),
+                                        cu_new.data_ptr(), seq_len.data_ptr(), ws, n,
+                                        _raw_stream(device.index)))
 
 
 def paged_gather_fp8(k_pages, k_scale, v_pages, v_scale, kidx_pages, kidx_scale, page_table,
@@ -892,31 +934,28 @@ def paged_gather_fp8(k_pages, k_scale, v_pages, v_scale, kidx_pages, kidx_scale,
     k_idx [T,d_idx]), where row t of sequence s (rows cu_rows[s] ..
     cu_rows[s+1]-1) is its position start[s] + t - cu_rows[s].  ``out``: the
     three tensors to write instead of new ones."""
-    device = k_pages.device
-    P, B_k, H_kv, d_h = _want_pages(k_pages, k_scale, v_pages, v_scale, device)
-    P2, B2, d_idx = _want_index_pages(kidx_pages, kidx_scale, device)
-    if (P2, B2) != (P, B_k):
-        raise ValueError(f"kidx_pages must hold {P} pages of {B_k} tokens, got {P2} of {B2}")
+    device = _device_of(k_pages, "k_pages", 4)
+    P, B_k, H_kv, d_h, d_idx = _want_pools(k_pages, k_scale, v_pages, v_scale, kidx_pages,
+                                           kidx_scale, device)
     S, max_pages = _want_seqs(cu_rows, start, page_table, device)
-    d = chunk_dims(S, T, max_pages, P, H_kv, H_kv, d_h, d_idx, B_k, 1)
     with _on(device, stream):
         if out is None:
-            k = torch.empty((T, H_kv, d_h), dtype=torch.bfloat16, device=device)
-            v = torch.empty((T, H_kv, d_h), dtype=torch.bfloat16, device=device)
-            k_idx = torch.empty((T, d_idx), dtype=torch.bfloat16, device=device)
+            k = torch.empty((T, H_kv, d_h), dtype=_BF16, device=device)
+            v = torch.empty((T, H_kv, d_h), dtype=_BF16, device=device)
+            k_idx = torch.empty((T, d_idx), dtype=_BF16, device=device)
         else:
             k, v, k_idx = out
-            _want(k, "k", torch.bfloat16, (T, H_kv, d_h))
-            _want(v, "v", torch.bfloat16, (T, H_kv, d_h))
-            _want(k_idx, "k_idx", torch.bfloat16, (T, d_idx))
-            _same_device(device, k=k, v=v, k_idx=k_idx)
+            _check(device, (k, "k", _BF16, (T, H_kv, d_h)), (v, "v", _BF16, (T, H_kv, d_h)),
+                   (k_idx, "k_idx", _BF16, (T, d_idx)))
         ws, n = _status_ws(workspace, device)
         _raise("msa_paged_gather_fp8",
-               LIB.msa_paged_gather_fp8(ctypes.byref(d), _ptr(k_pages), _ptr(k_scale),
-                                        _ptr(v_pages), _ptr(v_scale), _ptr(kidx_pages),
-                                        _ptr(kidx_scale), _ptr(page_table), _ptr(cu_rows),
-                                        _ptr(start), _ptr(k), _ptr(v), _ptr(k_idx), ws, n,
-                                        _stream(stream)))
+               LIB.msa_paged_gather_fp8(_chunk_ref(S, T, max_pages, P, H_kv, H_kv, d_h, d_idx, B_k, 1),
+                                        k_pages.data_ptr(), k_scale.data_ptr(), v_pages.data_ptr(),
+                                        v_scale.data_ptr(), kidx_pages.data_ptr(),
+                                        kidx_scale.data_ptr(), page_table.data_ptr(),
+                                        cu_rows.data_ptr(), start.data_ptr(), k.data_ptr(),
+                                        v.data_ptr(), k_idx.data_ptr(), ws, n,
+                                        _raw_stream(device.index)))
     return k, v, k_idx
 
 
@@ -927,25 +966,24 @@ def paged_index_scores_fp8(q_idx: torch.Tensor, kidx_pages, kidx_scale, page_tab
     q_idx [T,H_kv,d_idx] bf16 -> scores [T,H_kv,max_pages] fp32, -inf from each
     row's own block on.  The chunk's own keys are appended first
     (paged_append_fp8); seq_len is the cached length before the chunk."""
-    if not isinstance(q_idx, torch.Tensor) or q_idx.dim() != 3:
-        raise TypeError("q_idx must be a torch tensor [T, H_kv, d_idx]")
+    device = _device_of(q_idx, "q_idx", 3)
     T, H_kv, _ = q_idx.shape
-    device = q_idx.device
     P, B_k, d_idx = _want_index_pages(kidx_pages, kidx_scale, device)
-    _want(q_idx, "q_idx", torch.bfloat16, (T, H_kv, d_idx))
     S, max_pages = _want_seqs(cu_new, seq_len, page_table, device)
-    d = chunk_dims(S, T, max_pages, P, H_kv, H_kv, 64, d_idx, B_k, 1, idx_scale=idx_scale)
+    _check(device, (q_idx, "q_idx", _BF16, (T, H_kv, d_idx)))
     with _on(device, stream):
         if scores is None:
-            scores = torch.empty((T, H_kv, max_pages), dtype=torch.float32, device=device)
-        _want(scores, "scores", torch.float32, (T, H_kv, max_pages))
-        _same_device(device, scores=scores)
+            scores = torch.empty((T, H_kv, max_pages), dtype=_F32, device=device)
+        else:
+            _check(device, (scores, "scores", _F32, (T, H_kv, max_pages)))
         ws, n = _status_ws(workspace, device)
         _raise("msa_paged_index_scores_fp8",
-               LIB.msa_paged_index_scores_fp8(ctypes.byref(d), _ptr(q_idx), _ptr(kidx_pages),
-                                              _ptr(kidx_scale), _ptr(page_table), _ptr(cu_new),
-                                              _ptr(seq_len), _ptr(scores), ws, n,
-                                              _stream(stream)))
+               LIB.msa_paged_index_scores_fp8(_chunk_ref(S, T, max_pages, P, H_kv, H_kv, 64, d_idx, B_k,
+                                                         1, 0.0, idx_scale),
+                                              q_idx.data_ptr(), kidx_pages.data_ptr(),
+                                              kidx_scale.data_ptr(), page_table.data_ptr(),
+                                              cu_new.data_ptr(), seq_len.data_ptr(),
+                                              scores.data_ptr(), ws, n, _raw_stream(device.index)))
     return scores
 
 
@@ -955,25 +993,37 @@ def block_topk(scores: torch.Tensor, pos: torch.Tensor, B_k: int, k: int,
     (pos / B_k, pos [T] int32) and the k-1 best blocks before it, ties to the
     lower block, -inf and NaN never chosen -> idx [T,H_kv,k] int32, ascending,
     -1 padded.  Rows with pos < 0 are left as they were."""
-    if not isinstance(scores, torch.Tensor) or scores.dim() != 3:
-        raise TypeError("scores must be a torch tensor [T, H_kv, blocks]")
+    device = _device_of(scores, "scores", 3)
     T, H_kv, n = scores.shape
-    _want(scores, "scores", torch.float32, (T, H_kv, n))
-    _want(pos, "pos", torch.int32, (T,))
-    _same_device(scores.device, pos=pos, idx_out=idx_out)
-    d = chunk_dims(1, T, n, 1, H_kv, H_kv, 64, 64, B_k, k)
-    with _on(scores.device, stream):
+    _check(device, (scores, "scores", _F32, (T, H_kv, n)), (pos, "pos", _I32, (T,)))
+    with _on(device, stream):
         if idx_out is None:
-            idx_out = torch.empty((T, H_kv, k), dtype=torch.int32, device=scores.device)
-        _want(idx_out, "idx_out", torch.int32, (T, H_kv, k))
+            idx_out = torch.empty((T, H_kv, k), dtype=_I32, device=device)
+        else:
+            _check(device, (idx_out, "idx_out", _I32, (T, H_kv, k)))
         _raise("msa_block_topk",
-               LIB.msa_block_topk(ctypes.byref(d), _ptr(scores), _ptr(pos), _ptr(idx_out),
-                                  _stream(stream)))
+               LIB.msa_block_topk(_chunk_ref(1, T, n, 1, H_kv, H_kv, 64, 64, B_k, k),
+                                  scores.data_ptr(), pos.data_ptr(), idx_out.data_ptr(),
+                                  _raw_stream(device.index)))
     return idx_out
 
 
 def paged_sparse_attn_fp8_workspace_size(d: msa_chunk_dims) -> int:
     return int(LIB.msa_paged_sparse_attn_fp8_workspace(ctypes.byref(d)))
+
+
+def paged_chunk_fp8_workspace_size(d: msa_chunk_dims) -> int:
+    return int(LIB.msa_paged_chunk_fp8_workspace(ctypes.byref(d)))
+
+
+@functools.lru_cache(maxsize=1024)
+def _attn_bytes(device_index: int, *sizes) -> int:
+    return int(LIB.msa_paged_sparse_attn_fp8_workspace(_chunk_ref(*sizes)))
+
+
+@functools.lru_cache(maxsize=1024)
+def _chunk_bytes(device_index: int, *sizes) -> int:
+    return int(LIB.msa_paged_chunk_fp8_workspace(_chunk_ref(*sizes)))
 
 
 def paged_sparse_attn_fp8(q: torch.Tensor, idx: torch.Tensor, k_pages, k_scale, v_pages, v_scale,
@@ -985,39 +1035,33 @@ def paged_sparse_attn_fp8(q: torch.Tensor, idx: torch.Tensor, k_pages, k_scale, 
     idx [T,H_kv,k] int32 (blocks of each row's sequence) -> o [T,H_q,d_h] bf16
     and lse [T,H_q] fp32.  The chunk's own rows are in the cache already
     (paged_append_fp8); seq_len is the cached length before the chunk."""
-    if not isinstance(q, torch.Tensor) or q.dim() != 3:
-        raise TypeError("q must be a torch tensor [T, H_q, d_h]")
-    if not isinstance(idx, torch.Tensor) or idx.dim() != 3:
-        raise TypeError("idx must be a torch tensor [T, H_kv, k]")
+    device = _device_of(q, "q", 3)
+    _device_of(idx, "idx", 3)
     T, H_q, _ = q.shape
     kk = idx.shape[2]
-    device = q.device
     P, B_k, H_kv, d_h = _want_pages(k_pages, k_scale, v_pages, v_scale, device)
-    _want(q, "q", torch.bfloat16, (T, H_q, d_h))
-    _want(idx, "idx", torch.int32, (T, H_kv, kk))
     S, max_pages = _want_seqs(cu_new, seq_len, page_table, device)
-    _same_device(device, idx=idx, o=o, lse=lse, workspace=workspace)
-    d = chunk_dims(S, T, max_pages, P, H_q, H_kv, d_h, 64, B_k, kk, attn_scale=attn_scale)
+    _check(device, (q, "q", _BF16, (T, H_q, d_h)), (idx, "idx", _I32, (T, H_kv, kk)))
+    sizes = (S, T, max_pages, P, H_q, H_kv, d_h, 64, B_k, kk, attn_scale)
     with _on(device, stream):
         if o is None:
-            o = torch.empty((T, H_q, d_h), dtype=torch.bfloat16, device=device)
-        _want(o, "o", torch.bfloat16, (T, H_q, d_h))
-        if lse is None and want_lse:
-            lse = torch.empty((T, H_q), dtype=torch.float32, device=device)
+            o = torch.empty((T, H_q, d_h), dtype=_BF16, device=device)
+        else:
+            _check(device, (o, "o", _BF16, (T, H_q, d_h)))
         if lse is not None:
-            _want(lse, "lse", torch.float32, (T, H_q))
-        ws = _workspace(paged_sparse_attn_fp8_workspace_size(d), device, workspace)
+            _check(device, (lse, "lse", _F32, (T, H_q)))
+        elif want_lse:
+            lse = torch.empty((T, H_q), dtype=_F32, device=device)
+        ws = _scratch(_attn_bytes(device.index, *sizes), device, workspace)
         _raise("msa_paged_sparse_attn_fp8",
-               LIB.msa_paged_sparse_attn_fp8(ctypes.byref(d), _ptr(q), _ptr(idx), _ptr(k_pages),
-                                             _ptr(k_scale), _ptr(v_pages), _ptr(v_scale),
-                                             _ptr(page_table), _ptr(cu_new), _ptr(seq_len),
-                                             _ptr(o), _ptr(lse), _ptr(ws), ws.numel(),
-                                             _stream(stream)))
+               LIB.msa_paged_sparse_attn_fp8(_chunk_ref(*sizes), q.data_ptr(), idx.data_ptr(),
+                                             k_pages.data_ptr(), k_scale.data_ptr(),
+                                             v_pages.data_ptr(), v_scale.data_ptr(),
+                                             page_table.data_ptr(), cu_new.data_ptr(),
+                                             seq_len.data_ptr(), o.data_ptr(),
+                                             None if lse is None else lse.data_ptr(),
+                                             ws.data_ptr(), ws.numel(), _raw_stream(device.index)))
     return o, lse
-
-
-def paged_chunk_fp8_workspace_size(d: msa_chunk_dims) -> int:
-    return int(LIB.msa_paged_chunk_fp8_workspace(ctypes.byref(d)))
 
 
 def paged_chunk_fp8(q, q_idx, k_new, v_new, k_idx_new, k_pages, k_scale, v_pages, v_scale,
@@ -1032,40 +1076,36 @@ def paged_chunk_fp8(q, q_idx, k_new, v_new, k_idx_new, k_pages, k_scale, v_pages
     cu_new[s].  q [T,H_q,d_h], q_idx [T,H_kv,d_idx], k_new, v_new [T,H_kv,d_h],
     k_idx_new [T,d_idx] bf16.  Returns (o [T,H_q,d_h] bf16, lse [T,H_q] fp32 or
     None, idx [T,H_kv,kk] int32)."""
-    if not isinstance(q, torch.Tensor) or q.dim() != 3:
-        raise TypeError("q must be a torch tensor [T, H_q, d_h]")
+    device = _device_of(q, "q", 3)
     T, H_q, _ = q.shape
-    device = q.device
-    P, B_k, H_kv, d_h = _want_pages(k_pages, k_scale, v_pages, v_scale, device)
-    P2, B2, d_idx = _want_index_pages(kidx_pages, kidx_scale, device)
-    if (P2, B2) != (P, B_k):
-        raise ValueError(f"kidx_pages must hold {P} pages of {B_k} tokens, got {P2} of {B2}")
-    _want(q, "q", torch.bfloat16, (T, H_q, d_h))
-    _want(q_idx, "q_idx", torch.bfloat16, (T, H_kv, d_idx))
-    _want(k_new, "k_new", torch.bfloat16, (T, H_kv, d_h))
-    _want(v_new, "v_new", torch.bfloat16, (T, H_kv, d_h))
-    _want(k_idx_new, "k_idx_new", torch.bfloat16, (T, d_idx))
+    P, B_k, H_kv, d_h, d_idx = _want_pools(k_pages, k_scale, v_pages, v_scale, kidx_pages,
+                                           kidx_scale, device)
     S, max_pages = _want_seqs(cu_new, seq_len, page_table, device)
-    _same_device(device, q_idx=q_idx, k_new=k_new, v_new=v_new, k_idx_new=k_idx_new, o=o, lse=lse,
-                 idx_out=idx_out, workspace=workspace)
-    d = chunk_dims(S, T, max_pages, P, H_q, H_kv, d_h, d_idx, B_k, kk, attn_scale, idx_scale)
+    _check(device, (q, "q", _BF16, (T, H_q, d_h)), (q_idx, "q_idx", _BF16, (T, H_kv, d_idx)),
+           (k_new, "k_new", _BF16, (T, H_kv, d_h)), (v_new, "v_new", _BF16, (T, H_kv, d_h)),
+           (k_idx_new, "k_idx_new", _BF16, (T, d_idx)))
+    sizes = (S, T, max_pages, P, H_q, H_kv, d_h, d_idx, B_k, kk, attn_scale, idx_scale)
     with _on(device, stream):
         if o is None:
-            o = torch.empty((T, H_q, d_h), dtype=torch.bfloat16, device=device)
-        _want(o, "o", torch.bfloat16, (T, H_q, d_h))
-        if lse is None and want_lse:
-            lse = torch.empty((T, H_q), dtype=torch.float32, device=device)
+            o = torch.empty((T, H_q, d_h), dtype=_BF16, device=device)
+        else:
+            _check(device, (o, "o", _BF16, (T, H_q, d_h)))
         if lse is not None:
-            _want(lse, "lse", torch.float32, (T, H_q))
+            _check(device, (lse, "lse", _F32, (T, H_q)))
+        elif want_lse:
+            lse = torch.empty((T, H_q), dtype=_F32, device=device)
         if idx_out is None:
-            idx_out = torch.empty((T, H_kv, kk), dtype=torch.int32, device=device)
-        _want(idx_out, "idx_out", torch.int32, (T, H_kv, kk))
-        ws = _workspace(paged_chunk_fp8_workspace_size(d), device, workspace)
+            idx_out = torch.empty((T, H_kv, kk), dtype=_I32, device=device)
+        else:
+            _check(device, (idx_out, "idx_out", _I32, (T, H_kv, kk)))
+        ws = _scratch(_chunk_bytes(device.index, *sizes), device, workspace)
         _raise("msa_paged_chunk_fp8",
-               LIB.msa_paged_chunk_fp8(ctypes.byref(d), _ptr(q), _ptr(q_idx), _ptr(k_new),
-                                       _ptr(v_new), _ptr(k_idx_new), _ptr(k_pages), _ptr(k_scale),
-                                       _ptr(v_pages), _ptr(v_scale), _ptr(kidx_pages),
-                                       _ptr(kidx_scale), _ptr(page_table), _ptr(cu_new),
-                                       _ptr(seq_len), _ptr(o), _ptr(lse), _ptr(idx_out), _ptr(ws),
-                                       ws.numel(), _stream(stream)))
+               LIB.msa_paged_chunk_fp8(_chunk_ref(*sizes), q.data_ptr(), q_idx.data_ptr(),
+                                       k_new.data_ptr(), v_new.data_ptr(), k_idx_new.data_ptr(),
+                                       k_pages.data_ptr(), k_scale.data_ptr(), v_pages.data_ptr(),
+                                       v_scale.data_ptr(), kidx_pages.data_ptr(),
+                                       kidx_scale.data_ptr(), page_table.data_ptr(),
+                                       cu_new.data_ptr(), seq_len.data_ptr(), o.data_ptr(),
+                                       None if lse is None else lse.data_ptr(), idx_out.data_ptr(),
+                                       ws.data_ptr(), ws.numel(), _raw_stream(device.index)))
     return o, lse, idx_out
