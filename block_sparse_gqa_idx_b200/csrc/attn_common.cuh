@@ -93,6 +93,11 @@ struct InvParams {
   // packed sequences: per token {first token, first global block} of its
   // sequence; null for one sequence
   const int2* qinfo;
+  // paged cache: the page of every global block ({page, ...}, page -1 = none:
+  // its entries are dropped), and the blocks a sequence may have (an entry at
+  // or past it is reported); null / 0 otherwise
+  const int4* blk;
+  int64_t B_seq;
   int Tq;
   int Cw, W;  // queries per window, windows in the chunk
   ChunkBufs c;

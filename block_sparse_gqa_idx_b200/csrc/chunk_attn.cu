@@ -468,14 +468,33 @@ cudaError_t launch_direct(const AttendLaunch& a, cudaStream_t s) {
 
 }  // namespace
 
-size_t chunk_attend_workspace_bytes(int T, int H_q, int H_kv, int d_h, int B_k, int k) {
-  const int n = T > 0 ? splits_of(T, H_kv, B_k, k) : 1;
+// Which form.  The query-outer kernel's time is the bytes of the selected
+// pages as every row reads them (through L2); the KV-outer form costs about 30
+// us of short kernels and each page once, and pays from about 2^27 such values
+// on (H_q = 32, H_kv = 4, d_h = B_k = 128, k = 16: 128 rows).  Measured there,
+// query-outer against KV-outer, one sequence at 9K / at 61K: 64 rows 46 : 39 /
+// 50 : 83 us, 128 rows 68 : 47 / 76 : 90, 256 rows 106 : 56 / 114 : 93, 512 rows
+// 184 : 81 / 193 : 137; at d_h = B_k = 64, k = 8, 512 rows 43 : 43 / 45 : 88.
+static bool kv_outer(const msa::ChunkSeqs& c, int H_q, int H_kv, int d_h, int k) {
+  const int G = H_q / H_kv;
+  if (16 % G != 0 || (G < 8 && H_q % 8 != 0)) return false;  // its MMA rows and TMA boxes
+  if (static_cast<int64_t>(c.S) * c.max_pages * H_kv >= (int64_t(1) << 30)) return false;  // keys
+  if (c.n_pages * c.B_k >= (int64_t(1) << 31)) return false;  // TMA row coordinates
+  return static_cast<int64_t>(c.T) * H_kv * k * c.B_k * d_h >= (int64_t(1) << 27);
+}
+
+size_t chunk_attend_workspace_bytes(const ChunkSeqs& c, int H_q, int H_kv, int d_h, int k) {
+  if (c.T == 0) return 0;
+  if (kv_outer(c, H_q, H_kv, d_h, k))
+    return chunk_attend_kv_workspace_bytes(c.T, c.S, c.max_pages, H_q, H_kv, d_h, k);
+  const int n = splits_of(c.T, H_kv, c.B_k, k);
   if (n == 1) return 0;
-  const size_t rows = static_cast<size_t>(T) * H_q * n;
+  const size_t rows = static_cast<size_t>(c.T) * H_q * n;
   return align256(sizeof(float) * rows * d_h) + align256(sizeof(float) * rows);
 }
 
 cudaError_t launch_chunk_attend(const AttendLaunch& a, cudaStream_t s) {
+  if (kv_outer(a.c, a.H_q, a.H_kv, a.d_h, a.k)) return launch_chunk_attend_kv(a, s);
   if (a.d_h == 128)
     return a.c.B_k == 128 ? launch_direct<128, 128>(a, s) : launch_direct<128, 64>(a, s);
   return a.c.B_k == 128 ? launch_direct<64, 128>(a, s) : launch_direct<64, 64>(a, s);

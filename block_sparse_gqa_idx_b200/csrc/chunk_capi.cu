@@ -289,7 +289,8 @@ msa_status msa_block_topk(const msa_chunk_dims* d, const float* scores, const in
 size_t msa_paged_sparse_attn_fp8_workspace(const msa_chunk_dims* d) {
   if (check_chunk(d, true, false, true) != MSA_OK) return 0;
   return kStatusBytes +
-         msa::chunk_attend_workspace_bytes(d->T, d->H_q, d->H_kv, d->d_h, d->B_k, d->k);
+         msa::chunk_attend_workspace_bytes(chunk_seqs(d, nullptr, nullptr, nullptr), d->H_q,
+                                           d->H_kv, d->d_h, d->k);
 }
 
 msa_status msa_paged_sparse_attn_fp8(const msa_chunk_dims* d, const void* q, const int32_t* idx,
@@ -334,7 +335,8 @@ msa_status msa_paged_sparse_attn_fp8(const msa_chunk_dims* d, const void* q, con
 size_t msa_paged_chunk_fp8_workspace(const msa_chunk_dims* d) {
   if (check_chunk(d, true, true, true) != MSA_OK) return 0;
   return kStatusBytes + pos_bytes(d) + scores_bytes(d) +
-         msa::chunk_attend_workspace_bytes(d->T, d->H_q, d->H_kv, d->d_h, d->B_k, d->k);
+         msa::chunk_attend_workspace_bytes(chunk_seqs(d, nullptr, nullptr, nullptr), d->H_q,
+                                           d->H_kv, d->d_h, d->k);
 }
 
 msa_status msa_paged_chunk_fp8(const msa_chunk_dims* d, const void* q, const void* q_idx,

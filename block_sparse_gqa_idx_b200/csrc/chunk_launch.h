@@ -51,7 +51,11 @@ struct AttendLaunch {
   void* ws;  // chunk_attend_workspace_bytes
   DevStatus* status;
 };
-size_t chunk_attend_workspace_bytes(int T, int H_q, int H_kv, int d_h, int B_k, int k);
+size_t chunk_attend_workspace_bytes(const ChunkSeqs& c, int H_q, int H_kv, int d_h, int k);
 cudaError_t launch_chunk_attend(const AttendLaunch& a, cudaStream_t s);
+// The KV-outer form, for chunks of many rows (chunk_attn_kv.cu).
+size_t chunk_attend_kv_workspace_bytes(int T, int S, int max_pages, int H_q, int H_kv, int d_h,
+                                       int k);
+cudaError_t launch_chunk_attend_kv(const AttendLaunch& a, cudaStream_t s);
 
 }  // namespace msa

@@ -13,6 +13,23 @@
 namespace msa {
 namespace {
 
+// The key (r * B + global block) of query i's selection b in group r, or -1
+// when it selects nothing.
+__device__ __forceinline__ int inv_block(const InvParams& p, int64_t i, int r, int32_t b,
+                                         bool report_bad) {
+  if (b < -1 || b >= (p.B_seq > 0 ? p.B_seq : p.B)) {
+    if (report_bad) report(p.status, DEV_ERR_BAD_INDEX, 40, static_cast<int>(i), b);
+    return -1;
+  }
+  const int2 sq = seq_of(p.qinfo, i);
+  if (b < 0 || b > (i - sq.x) / p.B_k) return -1;
+  if (p.blk != nullptr && p.blk[sq.y + b].x < 0) {
+    if (report_bad) report(p.status, DEV_ERR_BAD_INDEX, 41, static_cast<int>(i), b);
+    return -1;
+  }
+  return r * static_cast<int>(p.B) + sq.y + b;
+}
+
 // The window-local key (r * B + global block) of entry e of the chunk, or -1
 // when the entry selects nothing (-1 padding, or a block after the query's
 // own).  Entry e is (query, group, slot) in the layout of I, so e is also the
@@ -23,12 +40,7 @@ __device__ __forceinline__ int inv_key(const InvParams& p, int64_t e, bool repor
   const int r = static_cast<int>((e - il * per_q) / p.kk);
   const int64_t i = p.q0 + il;
   const int32_t b = p.idx[p.q0 * per_q + e];
-  if (b < -1 || b >= p.B) {
-    if (report_bad) report(p.status, DEV_ERR_BAD_INDEX, 40, static_cast<int>(i), b);
-    return -1;
-  }
-  const int2 sq = seq_of(p.qinfo, i);
-  return (b >= 0 && b <= (i - sq.x) / p.B_k) ? r * static_cast<int>(p.B) + sq.y + b : -1;
+  return inv_block(p, i, r, b, report_bad);
 }
 
 // Inverse index with a per-CTA histogram of one window's keys in shared
@@ -94,12 +106,9 @@ __global__ void inv_index_kernel(const InvParams p) {
       const int64_t il = rem % p.nq;
       const int64_t i = p.q0 + il;
       const int32_t b = p.idx[(i * p.H_kv + r) * p.kk + s];
-      const int2 sq = seq_of(p.qinfo, i);
-      const int64_t b_i = (i - sq.x) / p.B_k;
-      if (b < -1 || b >= p.B) {
-        if (!SCATTER) report(p.status, DEV_ERR_BAD_INDEX, 40, static_cast<int>(i), b);
-      } else if (b >= 0 && b <= b_i) {
-        key = ((il / p.Cw) * p.H_kv + r) * p.B + sq.y + b;
+      const int local = inv_block(p, i, r, b, !SCATTER);
+      if (local >= 0) {
+        key = (il / p.Cw) * p.H_kv * p.B + local;
         slot = static_cast<uint32_t>((il * p.H_kv + r) * p.kk + s);
       }
     }

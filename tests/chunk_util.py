@@ -37,6 +37,7 @@ class Cache:
     seed: int = 0
     pad: int = 0   # padding rows behind the last sequence
     spare_pages: int = 3
+    wide: int = 0  # page-table entries per sequence, when more than needed
 
     def __post_init__(self):
         g = torch.Generator().manual_seed(1000 + self.seed)
@@ -44,7 +45,7 @@ class Cache:
         S, B = len(self.new), self.B_k
         self.S, self.T = S, sum(self.new) + self.pad
         need = [(n + h + B - 1) // B for n, h in zip(self.new, self.have)]
-        self.max_pages = max(1, max(need)) + 1
+        self.max_pages = max(max(need) + 1, self.wide)
         self.n_pages = sum(need) + self.spare_pages
         self.cu = torch.tensor([sum(self.new[:s]) for s in range(S + 1)], dtype=torch.int32)
         self.len = torch.tensor(self.have, dtype=torch.int32)

@@ -47,6 +47,13 @@ CASES = [  # new, have, B_k, H_kv, G, d_h, k, pad
     ([130, 1, 20], [0, 2000, 64], 128, 8, 2, 64, 6, 0),
     ([257], [10], 64, 4, 8, 64, 4, 5),
     ([300, 20], [500, 300], 128, 2, 8, 128, 5, 2),
+    # enough rows x selected keys for the KV-outer form
+    ([300, 20], [500, 300], 128, 4, 8, 128, 8, 2),
+    ([530], [10], 64, 8, 1, 64, 8, 0),
+    ([257, 0, 9], [1000, 5, 64], 128, 4, 16, 64, 16, 3),
+    ([200, 100, 1], [64, 2000, 700], 64, 8, 2, 128, 16, 0),
+    ([290], [0], 128, 2, 4, 128, 32, 1),
+    ([1] * 90 + [60] * 5, [130] * 95, 128, 4, 8, 128, 6, 0),
 ]
 
 
@@ -71,11 +78,11 @@ def test_against_float64(msa, new, have, B_k, H_kv, G, d_h, k, pad, holes):
     assert torch.equal(again[live], o[live])
 
 
-@pytest.mark.parametrize("new,have", [([1, 1], [700, 300]), ([200, 30], [300, 500])])
+@pytest.mark.parametrize("new,have", [([1, 1], [700, 300]), ([200, 30], [300, 500]), ([700, 30], [300, 500])])
 def test_scales_of_any_size(msa, new, have):
     """Value rows from 1e-20 to 1e15, a peaked softmax, large and tiny queries."""
-    c = Cache(new, have, 64, 2, 64, 64, seed=21)
-    q = torch.randn(c.T, 8, 64, generator=c.g).bfloat16()
+    c = Cache(new, have, 64, 2 if sum(new) < 700 else 4, 64, 64, seed=21)
+    q = torch.randn(c.T, 4 * c.H_kv, 64, generator=c.g).bfloat16()
     q[:, 1] *= 30.0
     q[:, 2] *= 2.0**-30
     mag = 10.0 ** torch.randint(-20, 16, (c.T,), generator=c.g).float()
@@ -87,14 +94,14 @@ def test_scales_of_any_size(msa, new, have):
     c.pool["v"][1][p, s] *= f[:, None]
     from tests.chunk_util import e4m3
     c.dense[0, "v"][: have[0]] = e4m3(c.pool["v"][0][p, s]) * c.pool["v"][1][p, s].double()[..., None]
-    idx = selection(c, 6)
+    idx = selection(c, 6 if sum(new) < 700 else 12)
     d = c.gpu(c.appended())
     o, lse = call(msa, c, d, q, idx, attn_scale=0.3)
     check(c, o, lse, attention(c, q, idx, 0.3))
 
 
-@pytest.mark.parametrize("new,have", [([3, 1], [100, 64]), ([140, 70], [100, 40])])
-def test_later_tokens_never_reach_a_row(msa, new, have):
+@pytest.mark.parametrize("new,have,k", [([3, 1], [100, 64], 3), ([140, 70], [100, 40], 3), ([440, 70], [900, 40], 17)])
+def test_later_tokens_never_reach_a_row(msa, new, have, k):
     """NaN and infinite rows of later tokens of the same chunk, and stale pages, leave earlier rows alone."""
     c = Cache(new, have, 64, 2, 128, 64, seed=31)
     q = torch.randn(c.T, 16, 128, generator=c.g).bfloat16()
@@ -102,7 +109,7 @@ def test_later_tokens_never_reach_a_row(msa, new, have):
     for n in "kv":
         c.rows[n][cut] = float("nan")
         c.rows[n][cut, 0, :3] = float("inf")
-    idx = selection(c, 3)
+    idx = selection(c, k)
     d = c.gpu(c.appended())
     for x in "kv":
         c.rows[x][cut] = 0.0  # the reference of the other rows does not see it
@@ -114,16 +121,17 @@ def test_later_tokens_never_reach_a_row(msa, new, have):
     assert bool(torch.isnan(o[cut]).all()) and bool(torch.isnan(lse[cut]).all())
 
 
-@pytest.mark.parametrize("new,have", [([1, 1], [400, 300]), ([150, 80], [400, 300])])
-def test_bad_pages_and_entries(msa, new, have):
-    c = Cache(new, have, 64, 2, 64, 64, seed=41)
-    q = torch.randn(c.T, 16, 64, generator=c.g).bfloat16()
-    idx = selection(c, 5)
+@pytest.mark.parametrize("new,have,H_kv,k", [([1, 1], [400, 300], 2, 5), ([150, 80], [400, 300], 2, 5),
+                                             ([250, 80], [400, 300], 8, 13)])
+def test_bad_pages_and_entries(msa, new, have, H_kv, k):
+    c = Cache(new, have, 64, H_kv, 64, 64, seed=41)
+    q = torch.randn(c.T, 8 * H_kv, 64, generator=c.g).bfloat16()
+    idx = selection(c, k)
     idx[:, 0, 0] = 1
     idx[:, 0, 1:3] = torch.tensor([0, 2], dtype=torch.int32)
     idx[:, 0, 3:] = -1
     d = c.gpu(c.appended())
-    ws = torch.zeros(64 << 20, dtype=torch.uint8, device="cuda")
+    ws = torch.zeros(256 << 20, dtype=torch.uint8, device="cuda")
     ref = attention(c, q, idx, 0.125)
     wrong = idx.clone()
     wrong[:, 0, 3] = c.max_pages       # outside: ignored, recorded
@@ -168,11 +176,11 @@ def test_equals_the_decode_step(msa):
     check(c, got, call(msa, c, d, q, idx)[1], ref)
 
 
-@pytest.mark.parametrize("new,have", [([1, 1], [400, 300]), ([150, 80], [400, 300])])
-def test_refusals_streams_and_graphs(msa, new, have):
+@pytest.mark.parametrize("new,have,k", [([1, 1], [400, 300], 5), ([150, 80], [400, 300], 5), ([650, 80], [400, 1300], 24)])
+def test_refusals_streams_and_graphs(msa, new, have, k):
     c = Cache(new, have, 64, 2, 64, 64, seed=61)
     q = torch.randn(c.T, 16, 64, generator=c.g).bfloat16()
-    idx = selection(c, 5)
+    idx = selection(c, k)
     d = c.gpu(c.appended())
     args = [q.cuda(), idx.cuda(), d["kp"], d["ks"], d["vp"], d["vs"], d["table"], d["cu"], d["len"]]
     for at, bad in ((0, q), (0, q.cuda().float()), (0, args[0][:, :15]), (1, args[1].long()), (1, args[1][:-1]),
@@ -193,7 +201,7 @@ def test_refusals_streams_and_graphs(msa, new, have):
         s.synchronize()
     assert all(torch.equal(a, b) for got in outs for a, b in zip(got, ref))
     # two captured calls that share the caller's workspace, replayed in turn
-    d_ = msa.chunk_dims(c.S, c.T, c.max_pages, c.n_pages, 16, 2, 64, 64, 64, 5)
+    d_ = msa.chunk_dims(c.S, c.T, c.max_pages, c.n_pages, 16, 2, 64, 64, 64, k)
     ws = torch.empty(msa.paged_sparse_attn_fp8_workspace_size(d_), dtype=torch.uint8, device="cuda")
     q2 = (args[0] * 0.5).contiguous()
     ref2 = msa.paged_sparse_attn_fp8(q2, *args[1:])
@@ -209,3 +217,39 @@ def test_refusals_streams_and_graphs(msa, new, have):
     torch.cuda.synchronize()
     for a, b in zip(got, (ref, ref2)):
         assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_wide_page_tables(msa):
+    """More (group, block) keys than one CTA scans: the same result as with a narrow table."""
+    c = Cache([300, 20, 40], [500, 300, 0], 128, 4, 128, 64, seed=91, wide=4096)
+    q = torch.randn(c.T, 32, 128, generator=c.g).bfloat16()
+    idx = selection(c, 8)
+    d = c.gpu(c.appended())
+    o, lse = call(msa, c, d, q, idx)
+    check(c, o, lse, attention(c, q, idx, 128**-0.5))
+    d["table"] = d["table"][:, :8].contiguous()
+    again, lse2 = call(msa, c, d, q, idx)
+    assert torch.equal(o, again) and torch.equal(lse, lse2)
+
+
+def test_more_rows_than_a_window(msa):
+    """A chunk longer than the window of rows whose partial results are held at once: what two calls give."""
+    T, cut, ctx = 131072 + 700, 131072 - 300, 1000
+    g = torch.Generator("cuda").manual_seed(5)
+    n_pages = (ctx + T + 63) // 64
+    kp, vp = (torch.randint(0, 120, (n_pages, 64, 1, 64), generator=g, device="cuda", dtype=torch.uint8) for _ in "kv")
+    ks, vs = (torch.rand(n_pages, 64, 1, generator=g, device="cuda") * 0.01 + 0.01 for _ in "kv")
+    q = torch.randn(T, 8, 64, generator=g, device="cuda").bfloat16()
+    pos = torch.arange(T, device="cuda") + ctx
+    own = pos // 64
+    early = (torch.rand(T, generator=g, device="cuda") * own).long()
+    idx = torch.stack([torch.minimum(early, own), torch.where(early < own, own, -1)], -1)[:, None].to(torch.int32).contiguous()
+    table = torch.arange(n_pages, device="cuda", dtype=torch.int32)[None]
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    o, lse = msa.paged_sparse_attn_fp8(q, idx, kp, ks, vp, vs, table, i32(0, T), i32(ctx))
+    parts = [msa.paged_sparse_attn_fp8(q[a:b].contiguous(), idx[a:b].contiguous(), kp, ks, vp, vs, table, i32(0, b - a),
+                                       i32(ctx + a)) for a, b in ((0, cut), (cut, T))]
+    assert bool(torch.isfinite(lse).all())
+    assert torch.equal(lse, torch.cat([p[1] for p in parts])) or float((lse - torch.cat([p[1] for p in parts])).abs().max()) < 1e-4
+    ref = torch.cat([p[0] for p in parts]).float()
+    assert float((o.float() - ref).abs().max()) <= 2.0**-7 * float(ref.abs().max())
