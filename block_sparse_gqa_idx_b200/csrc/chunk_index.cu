@@ -17,6 +17,24 @@
 namespace msa {
 namespace {
 
+// Bulk (untiled) copy global -> shared, counted on an mbarrier.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+// D (TMEM) [+]= A B, E4M3 operands in shared memory, K = 32.
+__device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                        uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
 struct ScoreParams {
   ChunkSeqs c;
   const __nv_bfloat16* q;  // [T, H_kv, d_idx]
@@ -173,6 +191,383 @@ __global__ void __launch_bounds__(256) chunk_scores_kernel(const ScoreParams p) 
   }
 }
 
+// ---------------------------------------------- scores on tcgen05, many rows --
+// For chunks with many rows: 256 rows (two UMMA M-tiles) against 128 keys at a
+// time, both in FP8: the codes go from their page by TMA straight into the
+// MMA's layout, and the queries are split into two E4M3 terms.  A row is scaled
+// by a power of two that puts its largest magnitude in [224, 448]; hi =
+// E4M3(x), lo = E4M3(x - hi) hold its 8 bits exactly down to 2^-10 of the
+// largest, and every element to 2^-18 of it.  hi and lo accumulate into the
+// same fp32 accumulators, so a tile costs what one bf16 product of the same
+// shape would.
+//   warp 0      page lookups, TMA of codes and of the keys' scales
+//   warp 1      MMAs, TMEM (two stages x two M-tiles x 128 columns)
+//   warps 4-7   the next unit's queries into hi and lo tiles
+//   warps 8-15  epilogue: two groups of four take the even and the odd key
+//               tiles; a thread has the same TMEM lane of both M-tiles, so a
+//               key's scale, read from shared memory as a broadcast, serves
+//               two rows; maxima wait in shared memory and leave eight tiles at
+//               a time, a row's values side by side.
+// A unit is (256 rows, CT key tiles); units are dealt out to one CTA per SM.
+// Rows of several sequences in one unit are taken one sequence after another
+// against the same query tiles.
+constexpr int kTcThreads = 512;
+constexpr int kRows = 256;   // rows per unit
+constexpr int kKeys = 128;   // keys per tile
+constexpr int kFlush = 8;    // tiles of a group between flushes
+
+struct TcParams {
+  ScoreParams s;
+  int rows;     // T * H_kv
+  int CT;       // key tiles per unit
+  int nchunk;   // units per 256 rows
+  int n_units;
+};
+
+template <int D, int BK>
+struct TcShape {
+  static constexpr int BPT = kKeys / BK;            // blocks per key tile
+  static constexpr int A_BYTES = kRows * D;         // hi (or lo) of a unit's rows
+  static constexpr int K_BYTES = kKeys * D;
+  static constexpr int ST = D == 64 ? 6 : 3;        // key tiles in flight
+  static constexpr uint32_t SWZ = D == 64 ? SW_64B : SW_128B;
+  static constexpr int SBO = 8 * D;                 // 8 rows
+  static constexpr int OUT = kFlush * BPT + 1;      // maxima per row (padded)
+  static constexpr size_t SMEM = 1024 + 2 * 2 * A_BYTES + ST * (K_BYTES + kKeys * 4) +
+                                 2 * kRows * OUT * 4 + 2 * kRows * 4 + ST * 4 +
+                                 (2 * ST + 8) * 8 + 64;
+  static_assert(SMEM <= 227 * 1024, "shared memory of one CTA");
+};
+
+// One sequence's rows of a unit.
+struct TcItem {
+  int s, ta;         // sequence, first token
+  int pos;           // its position
+  int own;           // the last token's own block
+  int ra, rb;        // rows of the unit
+  int k0, k1;        // key tiles to score
+};
+
+// Calls f for the items of unit u, in the same order in every role; stops when
+// f returns false.  `tell`: report sequences that do not fit.
+template <int BK, typename F>
+__device__ __forceinline__ void for_items(const TcParams& p, int u, bool tell, F f) {
+  constexpr int BPT = kKeys / BK;
+  const ChunkSeqs& c = p.s.c;
+  const int H = p.s.H_kv, m = u / p.nchunk, ch = u - m * p.nchunk;
+  const int R0 = m * kRows, R1 = min(R0 + kRows, p.rows);
+  const int t_end = (R1 - 1) / H + 1;
+  for (int t = R0 / H; t < t_end;) {
+    const ChunkTok tok = chunk_tok(c, t);
+    if (tok.pos < 0) {
+      if (tell && tok.too_long) report(p.s.status, DEV_ERR_CACHE_FULL, 202, tok.s, t);
+      ++t;
+      continue;
+    }
+    const int te = min(t_end, __ldg(c.cu + tok.s + 1));
+    TcItem it;
+    it.own = (tok.pos + te - t - 1) / BK;
+    it.s = tok.s;
+    it.ta = t;
+    it.pos = tok.pos;
+    it.ra = max(R0, t * H) - R0;
+    it.rb = min(R1, te * H) - R0;
+    it.k0 = ch * p.CT;
+    it.k1 = max(it.k0, min(it.k0 + p.CT, (it.own + BPT - 1) / BPT));
+    if (!f(it)) return;
+    t = te;
+  }
+}
+
+template <int D, int BK>
+__global__ void __launch_bounds__(kTcThreads, 1)
+    chunk_scores_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const TcParams p) {
+  using SH = TcShape<D, BK>;
+  constexpr int ST = SH::ST, BPT = SH::BPT;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint8_t* sA = smem;                          // [2] hi, lo of a unit's rows
+  uint8_t* sK = sA + 2 * 2 * SH::A_BYTES;      // [ST] codes
+  float* sS = reinterpret_cast<float*>(sK + ST * SH::K_BYTES);  // [ST][128] scales
+  float* sOut = sS + ST * kKeys;               // [2 groups][256][OUT] maxima
+  float* sRow = sOut + 2 * kRows * SH::OUT;    // [2] what a row's dots are multiplied with
+  int* sOk = reinterpret_cast<int*>(sRow + 2 * kRows);  // [ST] bit b: block b of the tile has a page
+  uint64_t* bars = reinterpret_cast<uint64_t*>(
+      (reinterpret_cast<uintptr_t>(sOk + ST) + 7) & ~static_cast<uintptr_t>(7));
+  uint64_t* k_full = bars;             // [ST]
+  uint64_t* k_empty = k_full + ST;     // [ST] MMAs done and scales read
+  uint64_t* a_full = k_empty + ST;     // [2]
+  uint64_t* a_empty = a_full + 2;      // [2] MMAs done and row factors read
+  uint64_t* acc_full = a_empty + 2;    // [2]
+  uint64_t* acc_empty = acc_full + 2;  // [2]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const ChunkSeqs& c = p.s.c;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int j = 0; j < ST; ++j) {
+      mbar_init(&k_full[j], 1);
+      mbar_init(&k_empty[j], 5);  // the MMAs' commit and the group's four warps
+    }
+    for (int j = 0; j < 2; ++j) {
+      mbar_init(&a_full[j], 4);
+      mbar_init(&a_empty[j], 9);  // the MMAs' commit and the eight epilogue warps
+      mbar_init(&acc_full[j], 1);
+      mbar_init(&acc_empty[j], 4);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) tmem_alloc(tmem_slot, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+
+  if (warp == 0) {
+    // -------------------------------------------------------- producer --
+    if (lane == 0) {
+      prefetch_tmap(&tm_k);
+      uint32_t g = 0;
+      bool ok = true;
+      for (int u = blockIdx.x; ok && u < p.n_units; u += gridDim.x)
+        for_items<BK>(p, u, true, [&](const TcItem& it) {
+          for (int kt = it.k0; ok && kt < it.k1; ++kt, ++g) {
+            const int st = g % ST;
+            ok = mbar_wait(&k_empty[st], ((g / ST) & 1) ^ 1, abort_flag, p.s.status, 200);
+            if (!ok) break;
+            int have = 0;
+            int64_t pg[BPT];
+#pragma unroll
+            for (int j = 0; j < BPT; ++j) {
+              const int b = kt * BPT + j;
+              pg[j] = b < c.max_pages ? chunk_page(c, it.s, b) : -1;
+              if (pg[j] < 0 && b < it.own)
+                report(p.s.status, DEV_ERR_BAD_INDEX, 201, it.s, b);
+              have |= pg[j] >= 0 ? 1 << j : 0;
+            }
+            sOk[st] = have;
+            mbar_arrive_expect_tx(&k_full[st], __popc(have) * (BK * D + BK * 4));
+#pragma unroll
+            for (int j = 0; j < BPT; ++j)
+              if (pg[j] >= 0) {
+                const int row = static_cast<int>(pg[j]) * BK;
+                tma_load_2d(sK + st * SH::K_BYTES + j * BK * D, &tm_k, &k_full[st], 0, row);
+                bulk_load(sS + st * kKeys + j * BK, p.s.scale + static_cast<int64_t>(row), BK * 4,
+                          &k_full[st]);
+              }
+          }
+          return ok;
+        });
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------- MMA --
+    if (lane == 0) {
+      // kind::f8f6f4, E4M3 x E4M3 -> f32, both K-major
+      constexpr uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(kKeys >> 3) << 17) | (128u >> 4 << 24);
+      const uint64_t a_desc = umma_desc(smem_u32(sA), 16, SH::SBO, SH::SWZ);
+      const uint64_t k_desc = umma_desc(smem_u32(sK), 16, SH::SBO, SH::SWZ);
+      uint32_t g = 0, ua = 0;
+      bool ok = true;
+      for (int u = blockIdx.x; ok && u < p.n_units; u += gridDim.x, ++ua) {
+        const int ab = ua & 1;
+        ok = mbar_wait(&a_full[ab], (ua >> 1) & 1, abort_flag, p.s.status, 210);
+        if (!ok) break;
+        const uint64_t ad0 = a_desc + ab * (2 * SH::A_BYTES >> 4);
+        for_items<BK>(p, u, false, [&](const TcItem& it) {
+          for (int kt = it.k0; ok && kt < it.k1; ++kt, ++g) {
+            const int st = g % ST, acc = g & 1;
+            ok = mbar_wait(&k_full[st], (g / ST) & 1, abort_flag, p.s.status, 211) &&
+                 mbar_wait(&acc_empty[acc], ((g >> 1) & 1) ^ 1, abort_flag, p.s.status, 212);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t kd = k_desc + st * (SH::K_BYTES >> 4);
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+              for (int term = 0; term < 2; ++term)
+#pragma unroll
+                for (int k = 0; k < D / 32; ++k)
+                  umma_f8(tmem_base + acc * 256 + mt * 128,
+                          ad0 + ((term * SH::A_BYTES + mt * 128 * D + k * 32) >> 4),
+                          kd + (k * 32 >> 4), idesc, (term | k) != 0);
+            umma_commit(&k_empty[st]);
+            umma_commit(&acc_full[acc]);
+          }
+          return ok;
+        });
+        umma_commit(&a_empty[ab]);
+      }
+      // the commits have arrived before the CTA ends
+      for (uint32_t j = ua > 2 ? ua - 2 : 0; ok && j < ua; ++j)
+        ok = mbar_wait(&a_empty[j & 1], (j >> 1) & 1, abort_flag, p.s.status, 213);
+    }
+  } else if (warp >= 4 && warp < 8) {
+    // ---------------------------------------------------------- queries --
+    // d/16 lanes per row, 16 values each
+    constexpr int LPR = D / 16, RPP = 128 / LPR;  // lanes per row, rows per pass
+    const int tid = threadIdx.x - 128, l = tid % LPR;
+    uint32_t ua = 0;
+    for (int u = blockIdx.x; u < p.n_units; u += gridDim.x, ++ua) {
+      const int ab = ua & 1;
+      if (!mbar_wait(&a_empty[ab], ((ua >> 1) & 1) ^ 1, abort_flag, p.s.status, 220)) break;
+      uint8_t* hi = sA + ab * 2 * SH::A_BYTES;
+      const int64_t R0 = static_cast<int64_t>(u / p.nchunk) * kRows;
+#pragma unroll 1
+      for (int r = tid / LPR; r < kRows; r += RPP) {
+        const bool on = R0 + r < p.rows;
+        const uint4* src = reinterpret_cast<const uint4*>(p.s.q + (R0 + (on ? r : 0)) * D) + 2 * l;
+        const uint4 raw[2] = {__ldg(src), __ldg(src + 1)};
+        float x[16], amax = 0.f;
+        const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(raw);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float2 f = __bfloat1622float2(h[e]);
+          x[2 * e] = f.x;
+          x[2 * e + 1] = f.y;
+          amax = fmax3(amax, fabsf(f.x), fabsf(f.y));
+        }
+#pragma unroll
+        for (int o = 1; o < LPR; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+        int shift = 0;
+        if (amax > 0.f && amax < INFINITY) {
+          shift = min(8 - ilogbf(amax), 126);
+          if (ldexpf(amax, shift) > 448.f) --shift;
+        }
+        uint32_t ch[4], cl[4];
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          uint32_t a = 0, b = 0;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float2 y = make_float2(ldexpf(x[4 * w + 2 * e], shift), ldexpf(x[4 * w + 2 * e + 1], shift));
+            const __nv_fp8x2_storage_t c2 = __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
+            const uint32_t back = widen2(c2);
+            const float2 z = __half22float2(*reinterpret_cast<const __half2*>(&back));
+            const __nv_fp8x2_storage_t d2 =
+                __nv_cvt_float2_to_fp8x2(make_float2(y.x - z.x, y.y - z.y), __NV_SATFINITE, __NV_E4M3);
+            a |= static_cast<uint32_t>(c2) << (16 * e);
+            b |= static_cast<uint32_t>(d2) << (16 * e);
+          }
+          ch[w] = a;
+          cl[w] = b;
+        }
+        // 16-byte chunk l of the row, swizzled as TMA would
+        const int chunk = D == 64 ? l ^ ((r >> 1) & 3) : l ^ (r & 7);
+        *reinterpret_cast<uint4*>(hi + r * D + chunk * 16) = make_uint4(ch[0], ch[1], ch[2], ch[3]);
+        *reinterpret_cast<uint4*>(hi + SH::A_BYTES + r * D + chunk * 16) =
+            make_uint4(cl[0], cl[1], cl[2], cl[3]);
+        if (l == 0) sRow[ab * kRows + r] = ldexpf(p.s.idx_scale, -shift);
+      }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&a_full[ab]);
+    }
+  } else if (warp >= 8) {
+    // --------------------------------------------------------- epilogue --
+    const int grp = (warp - 8) >> 2, quarter = warp & 3;
+    const int tl = quarter * 32 + lane;  // TMEM lane; rows tl and tl + 128
+    float* out_s = sOut + grp * kRows * SH::OUT;
+    const int H = p.s.H_kv, max_pages = c.max_pages;
+    uint32_t g = 0, ua = 0;
+    // after a wait that gave up, a warp goes the same way without waiting, so
+    // that the group's barriers still meet
+    bool ok = true;
+    for (int u = blockIdx.x; u < p.n_units; u += gridDim.x, ++ua) {
+      const int ab = ua & 1;
+      ok = ok && mbar_wait(&a_full[ab], (ua >> 1) & 1, abort_flag, p.s.status, 230);
+      const float* row_f = sRow + ab * kRows;
+      const int R0 = u / p.nchunk * kRows;
+      const int b_end = min((u % p.nchunk + 1) * p.CT * BPT, max_pages);  // of this unit's blocks
+      for_items<BK>(p, u, false, [&](const TcItem& it) {
+        // own block of the unit's row r
+        auto own_of = [&](int r) { return (it.pos + (R0 + r) / H - it.ta) / BK; };
+        auto dst = [&](int r) { return p.s.out + (static_cast<int64_t>(R0) + r) * max_pages; };
+        int held = 0, kt_first = 0;  // tiles of this group that wait in out_s: kt_first, + 2, ...
+        auto flush = [&] {
+          asm volatile("bar.sync %0, 128;" ::"r"(1 + grp) : "memory");
+          const int nv = held * BPT;
+          const int rows = it.rb - it.ra;
+          for (int i = tl; i < rows * nv; i += 128) {
+            const int r = it.ra + i / nv, v = i % nv;
+            const int b = (kt_first + 2 * (v / BPT)) * BPT + v % BPT;
+            if (b < b_end)
+              dst(r)[b] = b < own_of(r) ? out_s[r * SH::OUT + v] * row_f[r] : -INFINITY;
+          }
+          asm volatile("bar.sync %0, 128;" ::"r"(1 + grp) : "memory");
+          held = 0;
+        };
+        for (int kt = it.k0; kt < it.k1; ++kt, ++g) {
+          if ((g & 1) != grp) continue;
+          const int st = g % ST;
+          ok = ok && mbar_wait(&k_full[st], (g / ST) & 1, abort_flag, p.s.status, 231) &&
+               mbar_wait(&acc_full[grp], (g >> 1) & 1, abort_flag, p.s.status, 232);
+          ok = __all_sync(0xFFFFFFFFu, ok);
+          tc_fence_after();
+          const uint32_t ta = tmem_base + grp * 256 + (static_cast<uint32_t>(quarter * 32) << 16);
+          const float* sc = sS + st * kKeys;
+          const int have = sOk[st];
+          if (held == 0) kt_first = kt;
+          float m0 = -INFINITY, m1 = -INFINITY;
+#pragma unroll 1
+          for (int q = 0; q < kKeys / 32; ++q) {
+            uint32_t a[32], b[32];
+            tmem_ld32(ta + q * 32, a);
+            tmem_ld32(ta + 128 + q * 32, b);
+            tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 32; j += 4) {
+              const float4 s4 = *reinterpret_cast<const float4*>(sc + q * 32 + j);
+              const uint64_t s01 = f2_pack(s4.x, s4.y), s23 = f2_pack(s4.z, s4.w);
+              auto pair = [](const uint32_t (&v)[32], int i) {
+                return f2_pack(__uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+              };
+              const uint64_t x0 = f2_mul(pair(a, j), s01), x1 = f2_mul(pair(a, j + 2), s23);
+              const uint64_t y0 = f2_mul(pair(b, j), s01), y1 = f2_mul(pair(b, j + 2), s23);
+              m0 = fmax3(m0, f2_lo(x0), f2_hi(x0));
+              m0 = fmax3(m0, f2_lo(x1), f2_hi(x1));
+              m1 = fmax3(m1, f2_lo(y0), f2_hi(y0));
+              m1 = fmax3(m1, f2_lo(y1), f2_hi(y1));
+            }
+            if ((q + 1) % (BK / 32) == 0) {  // a block is complete
+              const int j = q / (BK / 32);
+              const bool on = (have >> j) & 1;
+              out_s[tl * SH::OUT + held * BPT + j] = on ? m0 : -INFINITY;
+              out_s[(tl + 128) * SH::OUT + held * BPT + j] = on ? m1 : -INFINITY;
+              m0 = m1 = -INFINITY;
+            }
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&acc_empty[grp]);
+            mbar_arrive(&k_empty[st]);
+          }
+          if (++held == kFlush) flush();
+        }
+        if (held > 0) flush();
+        // blocks that no row of the item scores
+        const int b0 = max(it.k0, it.k1) * BPT;
+        for (int r = it.ra + (warp - 8); r < it.rb; r += 8)
+          for (int b = b0 + lane; b < b_end; b += 32) dst(r)[b] = -INFINITY;
+        return true;
+      });
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&a_empty[ab]);
+    }
+  }
+
+  // every MMA is done once the epilogue has read its accumulators
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, 512);
+  }
+}
+
 // ------------------------------------------------------------------- top-k --
 struct TopkParams {
   const float* scores;  // [T, H_kv, n]
@@ -260,6 +655,12 @@ __global__ void __launch_bounds__(256) block_topk_kernel(const TopkParams p) {
   else if (lane < p.k) dst[lane] = -1;
 }
 
+// Which form (see chunk_scores_tc_kernel).
+bool scores_on_tc(const ScoreLaunch& a) {
+  if (a.c.n_pages * a.c.B_k >= (int64_t(1) << 31)) return false;  // TMA row coordinates
+  return static_cast<int64_t>(a.c.T) * a.H_kv >= 256;
+}
+
 template <int D, int BK>
 cudaError_t launch_scores_typed(const ScoreLaunch& a, cudaStream_t s) {
   ScoreParams p{};
@@ -272,6 +673,35 @@ cudaError_t launch_scores_typed(const ScoreLaunch& a, cudaStream_t s) {
   p.idx_scale = a.idx_scale;
   p.status = a.status;
   const int sms = num_sms();
+  if (scores_on_tc(a)) {
+    using SH = TcShape<D, BK>;
+    TcParams t{};
+    t.s = p;
+    t.rows = a.c.T * a.H_kv;
+    // about eight units per SM, of at least 16 key tiles, so that whole units
+    // even out over the SMs
+    const int m = (t.rows + kRows - 1) / kRows;
+    const int tiles = (a.c.max_pages + SH::BPT - 1) / SH::BPT;
+    const int want = (8 * sms + m - 1) / m;
+    t.CT = (tiles + want - 1) / want;
+    if (t.CT < 16) t.CT = 16;
+    t.nchunk = (tiles + t.CT - 1) / t.CT;
+    t.n_units = m * t.nchunk;
+    CUtensorMap tk;
+    // index keys as rows of D bytes (a map of 16-bit elements: only bytes move)
+    const uint64_t dims[2] = {static_cast<uint64_t>(D) / 2, static_cast<uint64_t>(a.c.n_pages) * BK};
+    const uint64_t strides[1] = {static_cast<uint64_t>(D)};
+    const uint32_t box[2] = {static_cast<uint32_t>(D) / 2, static_cast<uint32_t>(BK)};
+    if (!make_tmap_bf16(&tk, a.pages, 2, dims, strides, box, D)) return cudaErrorInvalidValue;
+    cudaError_t e = cudaFuncSetAttribute(chunk_scores_tc_kernel<D, BK>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(SH::SMEM));
+    if (e != cudaSuccess) return e;
+    prof_begin("chunk_scores_tc", s);
+    chunk_scores_tc_kernel<D, BK><<<t.n_units < sms ? t.n_units : sms, kTcThreads, SH::SMEM, s>>>(tk, t);
+    prof_end(s);
+    return cudaGetLastError();
+  }
   // Columns per tile: 8 while there are no more tokens than sequences (single
   // tokens share no keys), else 32.
   const bool wide = a.c.T > a.c.S && a.c.T * a.H_kv > 8;

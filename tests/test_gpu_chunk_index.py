@@ -56,6 +56,9 @@ CASES = [  # new, have, B_k, H_kv, d_idx, pad
     ([600], [1300], 128, 4, 128, 0),
     ([257, 400], [64, 2000], 64, 8, 64, 5),
     ([700, 1], [0, 3000], 128, 1, 64, 0),
+    ([100, 1, 90], [3000, 700, 0], 64, 3, 64, 4),
+    ([1] * 40 + [50] * 4, [260] * 44, 128, 5, 128, 0),
+    ([4, 4, 60, 300, 2], [5000, 128, 127, 64, 1], 128, 8, 128, 9),
 ]
 
 
@@ -81,7 +84,7 @@ def test_scores(msa, new, have, B_k, H_kv, d_idx, pad, scale):
     assert bool(((got - ref).abs()[~none] <= tol[~none]).all())
 
 
-@pytest.mark.parametrize("new,have", [([1, 1], [400, 400]), ([90, 50], [400, 300])])
+@pytest.mark.parametrize("new,have", [([1, 1], [400, 400]), ([30, 20], [400, 300]), ([90, 50], [400, 300])])
 def test_bad_pages_score_nothing(msa, new, have):
     c = Cache(new, have, 64, 4, 64, 64, seed=5)
     d = c.gpu(c.appended())
