@@ -234,7 +234,7 @@ struct TcShape {
   static constexpr int SBO = 8 * D;                 // 8 rows
   static constexpr int OUT = kFlush * BPT + 1;      // maxima per row (padded)
   static constexpr size_t SMEM = 1024 + 2 * 2 * A_BYTES + ST * (K_BYTES + kKeys * 4) +
-                                 2 * kRows * OUT * 4 + 2 * kRows * 4 + ST * 4 +
+                                 2 * kRows * OUT * 4 + 4 * kRows * 4 + ST * 4 +
                                  (2 * ST + 8) * 8 + 64;
   static_assert(SMEM <= 227 * 1024, "shared memory of one CTA");
 };
@@ -292,7 +292,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   float* sS = reinterpret_cast<float*>(sK + ST * SH::K_BYTES);  // [ST][128] scales
   float* sOut = sS + ST * kKeys;               // [2 groups][256][OUT] maxima
   float* sRow = sOut + 2 * kRows * SH::OUT;    // [2] what a row's dots are multiplied with
-  int* sOk = reinterpret_cast<int*>(sRow + 2 * kRows);  // [ST] bit b: block b of the tile has a page
+  int* sOwn = reinterpret_cast<int*>(sRow + 2 * kRows);  // [2 groups][256] own blocks
+  int* sOk = sOwn + 2 * kRows;  // [ST] bit b: block b of the tile has a page
   uint64_t* bars = reinterpret_cast<uint64_t*>(
       (reinterpret_cast<uintptr_t>(sOk + ST) + 7) & ~static_cast<uintptr_t>(7));
   uint64_t* k_full = bars;             // [ST]
@@ -470,6 +471,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const int grp = (warp - 8) >> 2, quarter = warp & 3;
     const int tl = quarter * 32 + lane;  // TMEM lane; rows tl and tl + 128
     float* out_s = sOut + grp * kRows * SH::OUT;
+    int* own_s = sOwn + grp * kRows;
     const int H = p.s.H_kv, max_pages = c.max_pages;
     uint32_t g = 0, ua = 0;
     // after a wait that gave up, a warp goes the same way without waiting, so
@@ -482,19 +484,21 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const int R0 = u / p.nchunk * kRows;
       const int b_end = min((u % p.nchunk + 1) * p.CT * BPT, max_pages);  // of this unit's blocks
       for_items<BK>(p, u, false, [&](const TcItem& it) {
-        // own block of the unit's row r
-        auto own_of = [&](int r) { return (it.pos + (R0 + r) / H - it.ta) / BK; };
-        auto dst = [&](int r) { return p.s.out + (static_cast<int64_t>(R0) + r) * max_pages; };
+        // the rows' own blocks, for the group's flushes
+#pragma unroll
+        for (int r = tl; r < kRows; r += 128) own_s[r] = (it.pos + (R0 + r) / H - it.ta) / BK;
         int held = 0, kt_first = 0;  // tiles of this group that wait in out_s: kt_first, + 2, ...
         auto flush = [&] {
+          constexpr int NV = kFlush * BPT;  // a row's values, one lane each
           asm volatile("bar.sync %0, 128;" ::"r"(1 + grp) : "memory");
-          const int nv = held * BPT;
-          const int rows = it.rb - it.ra;
-          for (int i = tl; i < rows * nv; i += 128) {
-            const int r = it.ra + i / nv, v = i % nv;
-            const int b = (kt_first + 2 * (v / BPT)) * BPT + v % BPT;
-            if (b < b_end)
-              dst(r)[b] = b < own_of(r) ? out_s[r * SH::OUT + v] * row_f[r] : -INFINITY;
+          const int v = tl % NV;
+          const int b = (kt_first + 2 * (v / BPT)) * BPT + v % BPT;
+          if (v < held * BPT && b < b_end) {
+            float* dst = p.s.out + static_cast<int64_t>(R0) * max_pages + b;
+#pragma unroll 4
+            for (int r = it.ra + tl / NV; r < it.rb; r += 128 / NV)
+              dst[static_cast<int64_t>(r) * max_pages] =
+                  b < own_s[r] ? out_s[r * SH::OUT + v] * row_f[r] : -INFINITY;
           }
           asm volatile("bar.sync %0, 128;" ::"r"(1 + grp) : "memory");
           held = 0;
@@ -550,8 +554,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (held > 0) flush();
         // blocks that no row of the item scores
         const int b0 = max(it.k0, it.k1) * BPT;
-        for (int r = it.ra + (warp - 8); r < it.rb; r += 8)
-          for (int b = b0 + lane; b < b_end; b += 32) dst(r)[b] = -INFINITY;
+        if (b0 < b_end)
+          for (int r = it.ra + (warp - 8); r < it.rb; r += 8) {
+            float* dst = p.s.out + (static_cast<int64_t>(R0) + r) * max_pages;
+            for (int b = b0 + lane; b < b_end; b += 32) dst[b] = -INFINITY;
+          }
+        asm volatile("bar.sync %0, 128;" ::"r"(1 + grp) : "memory");  // own_s is rewritten
         return true;
       });
       __syncwarp();
