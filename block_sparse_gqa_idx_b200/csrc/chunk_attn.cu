@@ -112,16 +112,17 @@ struct Attend {
       }
       amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
       amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
-      const int shift = amax > 0.f ? min(13 - ilogbf(amax), 126) : 0;
+      const int shift = amax > 0.f && amax < INFINITY ? min(13 - ilogbf(amax), 126) : 0;
+      const float up = pow2(shift);
 #pragma unroll
       for (int j = 0; j < NK; ++j) {
-        bq[n][j][0] = pack_f16(ldexpf(qv[j][0], shift), ldexpf(qv[j][1], shift));
-        bq[n][j][1] = pack_f16(ldexpf(qv[j][2], shift), ldexpf(qv[j][3], shift));
+        bq[n][j][0] = pack_f16(qv[j][0] * up, qv[j][1] * up);
+        bq[n][j][1] = pack_f16(qv[j][2] * up, qv[j][3] * up);
       }
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int sh = __shfl_sync(0xFFFFFFFFu, shift, (2 * t + e) * 4);
-        un[n][e] = ldexpf(p.scale_log2, -sh);
+        un[n][e] = p.scale_log2 * pow2(-sh);
         l[n][e] = 0.f;
         rx[n][e] = ry[n][e] = -INFINITY;
       }

@@ -12,6 +12,9 @@
 
 namespace msa {
 
+// 2^e, -126 <= e <= 127.
+__device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
+
 struct ChunkSeqs {
   const int32_t* cu;       // [S + 1]
   const int32_t* seq_len;  // [S] tokens cached before the chunk

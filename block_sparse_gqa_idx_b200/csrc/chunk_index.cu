@@ -104,18 +104,19 @@ __global__ void __launch_bounds__(256) chunk_scores_kernel(const ScoreParams p) 
       }
       amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
       amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
-      const int shift = amax > 0.f ? min(13 - ilogbf(amax), 126) : 0;
+      const int shift = amax > 0.f && amax < INFINITY ? min(13 - ilogbf(amax), 126) : 0;
+      const float up = pow2(shift);
 #pragma unroll
       for (int j = 0; j < NMMA; ++j) {
-        const __half2 lo = __floats2half2_rn(ldexpf(qv[j][0], shift), ldexpf(qv[j][1], shift));
-        const __half2 hi = __floats2half2_rn(ldexpf(qv[j][2], shift), ldexpf(qv[j][3], shift));
+        const __half2 lo = __floats2half2_rn(qv[j][0] * up, qv[j][1] * up);
+        const __half2 hi = __floats2half2_rn(qv[j][2] * up, qv[j][3] * up);
         bq[n][j][0] = *reinterpret_cast<const uint32_t*>(&lo);
         bq[n][j][1] = *reinterpret_cast<const uint32_t*>(&hi);
       }
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int sh = __shfl_sync(0xFFFFFFFFu, shift, (2 * t + e) * 4);
-        unscale[n][e] = ldexpf(p.idx_scale, -sh);
+        unscale[n][e] = p.idx_scale * pow2(-sh);
         const int cc = 8 * n + 2 * t + e;
         own[n][e] = cc < ncol ? (tok.pos + cc / p.H_kv) / BK : -1;
       }
@@ -329,40 +330,50 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
   if (warp == 0) {
     // -------------------------------------------------------- producer --
-    if (lane == 0) {
-      prefetch_tmap(&tm_k);
-      uint32_t g = 0;
-      bool ok = true;
-      for (int u = blockIdx.x; ok && u < p.n_units; u += gridDim.x)
-        for_items<BK>(p, u, true, [&](const TcItem& it) {
-          for (int kt = it.k0; ok && kt < it.k1; ++kt, ++g) {
-            const int st = g % ST;
-            ok = mbar_wait(&k_empty[st], ((g / ST) & 1) ^ 1, abort_flag, p.s.status, 200);
-            if (!ok) break;
-            int have = 0;
-            int64_t pg[BPT];
+    // Lane l holds the page of block l of a batch of 32, the next batch on its
+    // way; lane 0 waits and issues.
+    if (lane == 0) prefetch_tmap(&tm_k);
+    uint32_t g = 0;
+    bool ok = true;
+    for (int u = blockIdx.x; ok && u < p.n_units; u += gridDim.x)
+      for_items<BK>(p, u, true, [&](const TcItem& it) {
+        const int b0 = it.k0 * BPT, b1 = min(it.k1 * BPT, c.max_pages);
+        auto fetch = [&](int b) {
+          if (b >= b1) return -1;
+          const int pg = static_cast<int>(chunk_page(c, it.s, b));
+          if (pg < 0 && b < it.own) report(p.s.status, DEV_ERR_BAD_INDEX, 201, it.s, b);
+          return pg;
+        };
+        int mine = fetch(b0 + lane), next = fetch(b0 + 32 + lane);
+        for (int kt = it.k0; ok && kt < it.k1; ++kt, ++g) {
+          const int at = (kt - it.k0) * BPT % 32;
+          if (at == 0 && kt > it.k0) {
+            mine = next;
+            next = fetch(kt * BPT + 32 + lane);
+          }
+          int pg[BPT], have = 0;
 #pragma unroll
-            for (int j = 0; j < BPT; ++j) {
-              const int b = kt * BPT + j;
-              pg[j] = b < c.max_pages ? chunk_page(c, it.s, b) : -1;
-              if (pg[j] < 0 && b < it.own)
-                report(p.s.status, DEV_ERR_BAD_INDEX, 201, it.s, b);
-              have |= pg[j] >= 0 ? 1 << j : 0;
-            }
+          for (int j = 0; j < BPT; ++j) {
+            pg[j] = __shfl_sync(0xFFFFFFFFu, mine, at + j);
+            have |= pg[j] >= 0 ? 1 << j : 0;
+          }
+          const int st = g % ST;
+          ok = mbar_wait(&k_empty[st], ((g / ST) & 1) ^ 1, abort_flag, p.s.status, 200);
+          ok = __all_sync(0xFFFFFFFFu, ok);
+          if (ok && lane == 0) {
             sOk[st] = have;
             mbar_arrive_expect_tx(&k_full[st], __popc(have) * (BK * D + BK * 4));
 #pragma unroll
             for (int j = 0; j < BPT; ++j)
               if (pg[j] >= 0) {
-                const int row = static_cast<int>(pg[j]) * BK;
+                const int row = pg[j] * BK;
                 tma_load_2d(sK + st * SH::K_BYTES + j * BK * D, &tm_k, &k_full[st], 0, row);
-                bulk_load(sS + st * kKeys + j * BK, p.s.scale + static_cast<int64_t>(row), BK * 4,
-                          &k_full[st]);
+                bulk_load(sS + st * kKeys + j * BK, p.s.scale + row, BK * 4, &k_full[st]);
               }
           }
-          return ok;
-        });
-    }
+        }
+        return ok;
+      });
   } else if (warp == 1) {
     // ------------------------------------------------------------- MMA --
     if (lane == 0) {
@@ -435,15 +446,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         int shift = 0;
         if (amax > 0.f && amax < INFINITY) {
           shift = min(8 - ilogbf(amax), 126);
-          if (ldexpf(amax, shift) > 448.f) --shift;
+          if (amax * pow2(shift) > 448.f) --shift;
         }
+        const float up = pow2(shift);
         uint32_t ch[4], cl[4];
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
           uint32_t a = 0, b = 0;
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float2 y = make_float2(ldexpf(x[4 * w + 2 * e], shift), ldexpf(x[4 * w + 2 * e + 1], shift));
+            const float2 y = make_float2(x[4 * w + 2 * e] * up, x[4 * w + 2 * e + 1] * up);
             const __nv_fp8x2_storage_t c2 = __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
             const uint32_t back = widen2(c2);
             const float2 z = __half22float2(*reinterpret_cast<const __half2*>(&back));
@@ -460,7 +472,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         *reinterpret_cast<uint4*>(hi + r * D + chunk * 16) = make_uint4(ch[0], ch[1], ch[2], ch[3]);
         *reinterpret_cast<uint4*>(hi + SH::A_BYTES + r * D + chunk * 16) =
             make_uint4(cl[0], cl[1], cl[2], cl[3]);
-        if (l == 0) sRow[ab * kRows + r] = ldexpf(p.s.idx_scale, -shift);
+        if (l == 0) sRow[ab * kRows + r] = p.s.idx_scale * pow2(-shift);
       }
       fence_async_smem();
       __syncwarp();
