@@ -10,7 +10,17 @@
 // walks all earlier keys, a chunk writes its scores: a chunk has few rows, so
 // the keys are split over the SMs and no CTA sees a whole row.  M is small
 // beside the work (4 bytes per 2 * d_idx * B_k operations).
+//
+// Two forms, each with its own sequences of a batch (see kTcRows).  For single
+// tokens the bound is the cache's bytes: 32 x 32.7K keys, d_idx = 64 (71 MB),
+// 18.5 us, 3.8 TB/s; the rest is the launch, the look-ups and the last blocks of
+// warps that have one more than others.  For long chunks it is what the epilogue
+// does with the products, a multiplication by the key's scale and a maximum for
+// each: 4096 tokens of four groups x 61K keys take 236 us, 0.48 PFLOP/s (the
+// tensor cores do twice that: two terms per query).
 #include <cuda_fp8.h>
+
+#include <climits>
 
 #include "chunk_launch.h"
 
@@ -42,10 +52,73 @@ struct ScoreParams {
   const float* scale;      // [n_pages, B_k]
   float* out;              // [T, H_kv, max_pages]
   int H_kv;
-  int tpt;                 // tokens per CTA column tile
+  int tc_rows;             // sequences with this many rows are the tcgen05 kernel's
   float idx_scale;
   DevStatus* status;
 };
+
+// A sequence's rows of the call; n = 0 when it has none or does not fit.
+struct SeqRows {
+  int t0, n;  // first token, tokens
+  int pos;    // the first token's position
+};
+__device__ __forceinline__ SeqRows seq_rows(const ScoreParams& p, int s, int code) {
+  const int t0 = max(__ldg(p.c.cu + s), 0), t1 = min(__ldg(p.c.cu + s + 1), p.c.T);
+  if (t1 <= t0) return {0, 0, 0};
+  const int64_t len = __ldg(p.c.seq_len + s);
+  if (len < 0 || len + t1 - t0 > static_cast<int64_t>(p.c.max_pages) * p.c.B_k) {
+    if (code != 0) report(p.status, DEV_ERR_CACHE_FULL, code, s, t0);
+    return {0, 0, 0};
+  }
+  return {t0, t1 - t0, static_cast<int>(len)};
+}
+
+// Work items dealt out by sequence: the block's threads count the items of a
+// run of sequences each, and an item's sequence is found from the counts'
+// prefix sums.  `pre` is [blockDim.x + 1] in shared memory; all threads call.
+template <typename F>
+__device__ __forceinline__ int64_t seq_scan(int S, int64_t* pre, F count) {
+  const int per = (S + blockDim.x - 1) / blockDim.x, lane = threadIdx.x & 31;
+  int64_t mine = 0;
+  for (int j = 0; j < per; ++j) {
+    const int s = threadIdx.x * per + j;
+    if (s < S) mine += count(s);
+  }
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xFFFFFFFFu, mine, o);
+    if (lane >= o) mine += y;
+  }
+  pre[threadIdx.x + 1] = mine;
+  __syncthreads();
+  int64_t before = 0;  // the warps before this one
+  for (int w = 0; w < (threadIdx.x >> 5); ++w) before += pre[32 * w + 32];
+  __syncthreads();
+  pre[threadIdx.x + 1] = mine + before;
+  if (threadIdx.x == 0) pre[0] = 0;
+  __syncthreads();
+  return pre[blockDim.x];
+}
+// Item u's sequence; u becomes the item's number within it.
+template <typename F>
+__device__ __forceinline__ int seq_find(int S, const int64_t* pre, int64_t& u, F count) {
+  const int per = (S + blockDim.x - 1) / blockDim.x;
+  int lo = 0, hi = blockDim.x;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (pre[mid] <= u) lo = mid;
+    else hi = mid;
+  }
+  u -= pre[lo];
+  if (per == 1) return lo;
+  int s = lo * per;
+  for (; s < S - 1; ++s) {
+    const int64_t n = count(s);
+    if (u < n) break;
+    u -= n;
+  }
+  return s;
+}
 
 // Two E4M3 codes -> an f16 pair (exact), one conversion instruction.
 __device__ __forceinline__ uint32_t widen2(uint32_t c2) {
@@ -54,141 +127,166 @@ __device__ __forceinline__ uint32_t widen2(uint32_t c2) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Scores on mma.sync, straight from global memory.  MMA rows = 16 keys, whose
-// codes widen to f16 in registers; columns = the (token, group) rows of the
-// CTA's tpt tokens, NT tiles of 8.  The d axis is consumed in a per-thread
-// order (thread t of a quad owns d in [t*D/4, (t+1)*D/4)), the same for keys
-// and queries.  A query enters as f16 times a power of two that puts its
-// largest magnitude in [2^13, 2^14): exact for every value within 2^-30 of
-// it.  One warp scores one block at a time, the blocks strided over the grid's
-// x; each key byte is read once per column tile.
+// Scores on mma.sync, straight from global memory, for sequences with few rows.
+// MMA rows = 16 keys, whose codes widen to f16 in registers; columns = the
+// (token, group) rows of one sequence's tokens, NT tiles of 8.  The d axis is
+// consumed in a per-thread order (thread t of a quad owns d in [t*D/4,
+// (t+1)*D/4)), the same for keys and queries.  A query enters as f16 times a
+// power of two that puts its largest magnitude in [2^13, 2^14): exact for every
+// value within 2^-30 of it.  One warp scores one block at a time; each key byte
+// is read once per column tile.
 template <int D, int BK, int NT>
-__global__ void __launch_bounds__(256) chunk_scores_kernel(const ScoreParams p) {
+__device__ __forceinline__ void scores_tile(const ScoreParams& p, int s, int ta, int tokens,
+                                            int pos, int b_first, int b_step) {
   constexpr int DT = D / 4;     // codes per thread and key row
   constexpr int NMMA = D / 16;  // MMAs per 16-key tile
   constexpr int NU = DT / 16;   // 16-byte loads per thread and key row
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
-  const int t_end = min(p.c.T, static_cast<int>(blockIdx.y + 1) * p.tpt);
-  // the tile's tokens, one sequence's run at a time
-  for (int ta = blockIdx.y * p.tpt; ta < t_end;) {
-    const ChunkTok tok = chunk_tok(p.c, ta);
-    if (tok.pos < 0) {
-      if (tok.too_long && blockIdx.x == 0 && threadIdx.x == 0)
-        report(p.status, DEV_ERR_CACHE_FULL, 120, tok.s, ta);
-      ++ta;
-      continue;
+  const int ncol = tokens * p.H_kv;
+  const int64_t row0 = static_cast<int64_t>(ta) * p.H_kv;
+  uint32_t bq[NT][NMMA][2];
+  float unscale[NT][2];  // of columns 2t, 2t + 1
+  int own[NT][2];        // their tokens' own blocks (-1 past the columns)
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const int col = 8 * n + g;
+    const __nv_bfloat16* qr = p.q + (row0 + (col < ncol ? col : 0)) * D;
+    float qv[NMMA][4], amax = 0.f;
+#pragma unroll
+    for (int j = 0; j < NMMA; ++j) {
+      const uint2 raw = __ldg(reinterpret_cast<const uint2*>(qr + t * DT + 4 * j));
+      const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&raw.x));
+      const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&raw.y));
+      qv[j][0] = a.x;
+      qv[j][1] = a.y;
+      qv[j][2] = b.x;
+      qv[j][3] = b.y;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) amax = fmaxf(amax, fabsf(qv[j][e]));
     }
-    const int tb = min(t_end, __ldg(p.c.cu + tok.s + 1));
-    const int ncol = (tb - ta) * p.H_kv;
-    const int64_t row0 = static_cast<int64_t>(ta) * p.H_kv;
-    uint32_t bq[NT][NMMA][2];
-    float unscale[NT][2];  // of columns 2t, 2t + 1
-    int own[NT][2];        // their tokens' own blocks (-1 past the columns)
+    amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
+    amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
+    const int shift = amax > 0.f && amax < INFINITY ? min(13 - ilogbf(amax), 126) : 0;
+    const float up = pow2(shift);
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const int col = 8 * n + g;
-      const __nv_bfloat16* qr = p.q + (row0 + (col < ncol ? col : 0)) * D;
-      float qv[NMMA][4], amax = 0.f;
-#pragma unroll
-      for (int j = 0; j < NMMA; ++j) {
-        const uint2 raw = __ldg(reinterpret_cast<const uint2*>(qr + t * DT + 4 * j));
-        const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&raw.x));
-        const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&raw.y));
-        qv[j][0] = a.x;
-        qv[j][1] = a.y;
-        qv[j][2] = b.x;
-        qv[j][3] = b.y;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) amax = fmaxf(amax, fabsf(qv[j][e]));
-      }
-      amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
-      amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
-      const int shift = amax > 0.f && amax < INFINITY ? min(13 - ilogbf(amax), 126) : 0;
-      const float up = pow2(shift);
-#pragma unroll
-      for (int j = 0; j < NMMA; ++j) {
-        const __half2 lo = __floats2half2_rn(qv[j][0] * up, qv[j][1] * up);
-        const __half2 hi = __floats2half2_rn(qv[j][2] * up, qv[j][3] * up);
-        bq[n][j][0] = *reinterpret_cast<const uint32_t*>(&lo);
-        bq[n][j][1] = *reinterpret_cast<const uint32_t*>(&hi);
-      }
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int sh = __shfl_sync(0xFFFFFFFFu, shift, (2 * t + e) * 4);
-        unscale[n][e] = p.idx_scale * pow2(-sh);
-        const int cc = 8 * n + 2 * t + e;
-        own[n][e] = cc < ncol ? (tok.pos + cc / p.H_kv) / BK : -1;
-      }
+    for (int j = 0; j < NMMA; ++j) {
+      const __half2 lo = __floats2half2_rn(qv[j][0] * up, qv[j][1] * up);
+      const __half2 hi = __floats2half2_rn(qv[j][2] * up, qv[j][3] * up);
+      bq[n][j][0] = *reinterpret_cast<const uint32_t*>(&lo);
+      bq[n][j][1] = *reinterpret_cast<const uint32_t*>(&hi);
     }
-    const int last = (tok.pos + tb - ta - 1) / BK;  // own block of the run's last token
-    float* out = p.out + row0 * p.c.max_pages;
-    for (int b = blockIdx.x * 8 + warp; b < p.c.max_pages; b += gridDim.x * 8) {
-      float mx[NT][2];
 #pragma unroll
-      for (int n = 0; n < NT; ++n) mx[n][0] = mx[n][1] = -INFINITY;
-      const int64_t pg = b < last ? chunk_page(p.c, tok.s, b) : -1;
-      if (b < last && pg < 0 && lane == 0) report(p.status, DEV_ERR_BAD_INDEX, 121, tok.s, b);
-      if (pg >= 0) {
-        const uint8_t* kbase = p.pages + (pg * BK + g) * D + t * DT;
-        const float* sbase = p.scale + pg * BK + g;
-        // the block in halves: a half's codes are all loaded before its MMAs
-        constexpr int HALF = BK / 32;
+    for (int e = 0; e < 2; ++e) {
+      const int sh = __shfl_sync(0xFFFFFFFFu, shift, (2 * t + e) * 4);
+      unscale[n][e] = p.idx_scale * pow2(-sh);
+      const int cc = 8 * n + 2 * t + e;
+      own[n][e] = cc < ncol ? (pos + cc / p.H_kv) / BK : -1;
+    }
+  }
+  const int last = (pos + tokens - 1) / BK;  // own block of the last token
+  float* out = p.out + row0 * p.c.max_pages;
+  for (int b = b_first; b < p.c.max_pages; b += b_step) {
+    float mx[NT][2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint4 cr[HALF][2][NU];
-          float sc[HALF][2];
+    for (int n = 0; n < NT; ++n) mx[n][0] = mx[n][1] = -INFINITY;
+    const int64_t pg = b < last ? chunk_page(p.c, s, b) : -1;
+    if (b < last && pg < 0 && lane == 0) report(p.status, DEV_ERR_BAD_INDEX, 121, s, b);
+    if (pg >= 0) {
+      const uint8_t* kbase = p.pages + (pg * BK + g) * D + t * DT;
+      const float* sbase = p.scale + pg * BK + g;
+      // the block in parts: a part's codes are all loaded before its MMAs
+      constexpr int PARTS = NT == 1 ? 4 : D / 32;
+      constexpr int KT = BK / 16 / PARTS;  // 16-key tiles of a part
+#pragma unroll 1
+      for (int h = 0; h < PARTS; ++h) {
+        uint4 cr[KT][2][NU];
+        float sc[KT][2];
 #pragma unroll
-          for (int i = 0; i < HALF; ++i)
+        for (int i = 0; i < KT; ++i)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int key = (h * HALF + i) * 16 + 8 * e;
+          for (int e = 0; e < 2; ++e) {
+            const int key = (h * KT + i) * 16 + 8 * e;
 #pragma unroll
-              for (int u = 0; u < NU; ++u)
-                cr[i][e][u] = __ldg(reinterpret_cast<const uint4*>(kbase + key * D) + u);
-              sc[i][e] = __ldg(sbase + key);
-            }
+            for (int u = 0; u < NU; ++u)
+              cr[i][e][u] = __ldg(reinterpret_cast<const uint4*>(kbase + key * D) + u);
+            sc[i][e] = __ldg(sbase + key);
+          }
 #pragma unroll
-          for (int i = 0; i < HALF; ++i) {
-            float acc[NT][4];
+        for (int i = 0; i < KT; ++i) {
+          float acc[NT][4];
 #pragma unroll
-            for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
+          for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
 #pragma unroll
-            for (int j = 0; j < NMMA; ++j) {
-              // k-slots 2t,2t+1 <- d0,d0+1 ; 2t+8,2t+9 <- d0+2,d0+3 (d0 = t*DT + 4j)
-              const uint32_t w0 = reinterpret_cast<const uint32_t*>(cr[i][0])[j];
-              const uint32_t w1 = reinterpret_cast<const uint32_t*>(cr[i][1])[j];
-              const uint32_t a[4] = {widen2(w0), widen2(w1), widen2(w0 >> 16), widen2(w1 >> 16)};
+          for (int j = 0; j < NMMA; ++j) {
+            // k-slots 2t,2t+1 <- d0,d0+1 ; 2t+8,2t+9 <- d0+2,d0+3 (d0 = t*DT + 4j)
+            const uint32_t w0 = reinterpret_cast<const uint32_t*>(cr[i][0])[j];
+            const uint32_t w1 = reinterpret_cast<const uint32_t*>(cr[i][1])[j];
+            const uint32_t a[4] = {widen2(w0), widen2(w1), widen2(w0 >> 16), widen2(w1 >> 16)};
 #pragma unroll
-              for (int n = 0; n < NT; ++n) mma_f16_16816(acc[n], a, bq[n][j][0], bq[n][j][1]);
-            }
+            for (int n = 0; n < NT; ++n) mma_f16_16816(acc[n], a, bq[n][j][0], bq[n][j][1]);
+          }
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              mx[n][0] = fmax3(mx[n][0], (acc[n][0] * unscale[n][0]) * sc[i][0],
-                               (acc[n][2] * unscale[n][0]) * sc[i][1]);
-              mx[n][1] = fmax3(mx[n][1], (acc[n][1] * unscale[n][1]) * sc[i][0],
-                               (acc[n][3] * unscale[n][1]) * sc[i][1]);
-            }
+          for (int n = 0; n < NT; ++n) {
+            mx[n][0] = fmax3(mx[n][0], (acc[n][0] * unscale[n][0]) * sc[i][0],
+                             (acc[n][2] * unscale[n][0]) * sc[i][1]);
+            mx[n][1] = fmax3(mx[n][1], (acc[n][1] * unscale[n][1]) * sc[i][0],
+                             (acc[n][3] * unscale[n][1]) * sc[i][1]);
           }
         }
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-#pragma unroll
-            for (int o = 4; o < 32; o <<= 1)
-              mx[n][e] = fmaxf(mx[n][e], __shfl_xor_sync(0xFFFFFFFFu, mx[n][e], o));
       }
-      if (g == 0)
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int e = 0; e < 2; ++e)
-            if (own[n][e] >= 0)
-              out[static_cast<int64_t>(8 * n + 2 * t + e) * p.c.max_pages + b] =
-                  b < own[n][e] ? mx[n][e] : -INFINITY;
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1)
+            mx[n][e] = fmaxf(mx[n][e], __shfl_xor_sync(0xFFFFFFFFu, mx[n][e], o));
     }
-    ta = tb;
+    if (g == 0)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          if (own[n][e] >= 0)
+            out[static_cast<int64_t>(8 * n + 2 * t + e) * p.c.max_pages + b] =
+                b < own[n][e] ? mx[n][e] : -INFINITY;
+  }
+}
+
+// Units are (a column tile of one sequence, a share of the blocks), dealt out
+// to the grid; a tile's blocks are split so that the units fill it.
+template <int D, int NT>
+constexpr int kHeld = NT == 1 ? 4 : D == 64 ? 2 : 1;  // CTAs per SM
+template <int D, int BK, int NT>
+__global__ void __launch_bounds__(256, kHeld<D, NT>) chunk_scores_kernel(const ScoreParams p) {
+  __shared__ int64_t pre[257];
+  griddep_wait();
+  const int tpt = 8 * NT / p.H_kv, code = blockIdx.x == 0 ? 120 : 0;
+  const auto count_of = [&](const SeqRows& r) {
+    return static_cast<int64_t>(r.n) * p.H_kv < p.tc_rows ? (r.n + tpt - 1) / tpt : 0;
+  };
+  const auto count = [&](int s) { return count_of(seq_rows(p, s, 0)); };
+  // (no more than T unless cu is not a sequence of offsets)
+  const int tiles = static_cast<int>(min(
+      seq_scan(p.c.S, pre, [&](int s) { return count_of(seq_rows(p, s, code)); }),
+      static_cast<int64_t>(p.c.T)));
+  if (tiles == 0) return;
+  const int grid = gridDim.x;
+  int split = grid / tiles;
+  if (split < 4) split = min((p.c.max_pages + 31) / 32, (4 * grid + tiles - 1) / tiles);
+  split = max(1, min(split, (p.c.max_pages + 7) / 8));
+  const int warp = threadIdx.x >> 5;
+  for (int64_t u = blockIdx.x; u < static_cast<int64_t>(tiles) * split; u += grid) {
+    int64_t tile = u / split;
+    const int x = static_cast<int>(u - tile * split);
+    const int s = seq_find(p.c.S, pre, tile, count);
+    const SeqRows r = seq_rows(p, s, 0);
+    const int first = static_cast<int>(tile) * tpt, n = min(tpt, r.n - first);
+    if (NT == 1 || n * p.H_kv <= 8)
+      scores_tile<D, BK, 1>(p, s, r.t0 + first, n, r.pos + first, x * 8 + warp, split * 8);
+    else
+      scores_tile<D, BK, NT>(p, s, r.t0 + first, n, r.pos + first, x * 8 + warp, split * 8);
   }
 }
 
@@ -198,7 +296,7 @@ __global__ void __launch_bounds__(256) chunk_scores_kernel(const ScoreParams p) 
 // MMA's layout, and the queries are split into two E4M3 terms.  A row is scaled
 // by a power of two that puts its largest magnitude in [224, 448]; hi =
 // E4M3(x), lo = E4M3(x - hi) hold its 8 bits exactly down to 2^-10 of the
-// largest, and every element to 2^-18 of it.  hi and lo accumulate into the
+// largest, and every element to 2^-10 / 224 of it.  hi and lo accumulate into the
 // same fp32 accumulators, so a tile costs what one bf16 product of the same
 // shape would.
 //   warp 0      page lookups, TMA of codes and of the keys' scales
@@ -209,21 +307,12 @@ __global__ void __launch_bounds__(256) chunk_scores_kernel(const ScoreParams p) 
 //               key's scale, read from shared memory as a broadcast, serves
 //               two rows; maxima wait in shared memory and leave eight tiles at
 //               a time, a row's values side by side.
-// A unit is (256 rows, CT key tiles); units are dealt out to one CTA per SM.
-// Rows of several sequences in one unit are taken one sequence after another
-// against the same query tiles.
+// A unit is (256 rows of one sequence, CT key tiles); units are dealt out to one
+// CTA per SM, about eight to each so that whole units even out.
 constexpr int kTcThreads = 512;
 constexpr int kRows = 256;   // rows per unit
 constexpr int kKeys = 128;   // keys per tile
 constexpr int kFlush = 8;    // tiles of a group between flushes
-
-struct TcParams {
-  ScoreParams s;
-  int rows;     // T * H_kv
-  int CT;       // key tiles per unit
-  int nchunk;   // units per 256 rows
-  int n_units;
-};
 
 template <int D, int BK>
 struct TcShape {
@@ -236,53 +325,76 @@ struct TcShape {
   static constexpr int OUT = kFlush * BPT + 1;      // maxima per row (padded)
   static constexpr size_t SMEM = 1024 + 2 * 2 * A_BYTES + ST * (K_BYTES + kKeys * 4) +
                                  2 * kRows * OUT * 4 + 4 * kRows * 4 + ST * 4 +
-                                 (2 * ST + 8) * 8 + 64;
+                                 (2 * ST + 8) * 8 + 64 + (kTcThreads + 1) * 8;
   static_assert(SMEM <= 227 * 1024, "shared memory of one CTA");
 };
 
-// One sequence's rows of a unit.
-struct TcItem {
-  int s, ta;         // sequence, first token
-  int pos;           // its position
-  int own;           // the last token's own block
-  int ra, rb;        // rows of the unit
+struct TcUnit {
+  int s;
+  int64_t row0;      // first row of the call
+  int rows;          // rows of the unit
+  int first;         // the unit's first row within its sequence
+  int pos;           // position of the sequence's first row
+  int own;           // the last row's own block
   int k0, k1;        // key tiles to score
+  int b_end;         // end of the blocks that the unit writes
 };
 
-// Calls f for the items of unit u, in the same order in every role; stops when
-// f returns false.  `tell`: report sequences that do not fit.
-template <int BK, typename F>
-__device__ __forceinline__ void for_items(const TcParams& p, int u, bool tell, F f) {
-  constexpr int BPT = kKeys / BK;
-  const ChunkSeqs& c = p.s.c;
-  const int H = p.s.H_kv, m = u / p.nchunk, ch = u - m * p.nchunk;
-  const int R0 = m * kRows, R1 = min(R0 + kRows, p.rows);
-  const int t_end = (R1 - 1) / H + 1;
-  for (int t = R0 / H; t < t_end;) {
-    const ChunkTok tok = chunk_tok(c, t);
-    if (tok.pos < 0) {
-      if (tell && tok.too_long) report(p.s.status, DEV_ERR_CACHE_FULL, 202, tok.s, t);
-      ++t;
-      continue;
-    }
-    const int te = min(t_end, __ldg(c.cu + tok.s + 1));
-    TcItem it;
-    it.own = (tok.pos + te - t - 1) / BK;
-    it.s = tok.s;
-    it.ta = t;
-    it.pos = tok.pos;
-    it.ra = max(R0, t * H) - R0;
-    it.rb = min(R1, te * H) - R0;
-    it.k0 = ch * p.CT;
-    it.k1 = max(it.k0, min(it.k0 + p.CT, (it.own + BPT - 1) / BPT));
-    if (!f(it)) return;
-    t = te;
+// How the call's units are laid out: the same in every role.
+template <int BK>
+struct TcPlan {
+  static constexpr int BPT = kKeys / BK;
+  const ScoreParams& p;
+  const int64_t* pre;
+  int CT;
+  int64_t units;
+
+  __device__ __forceinline__ bool has(const SeqRows& r) const {
+    return static_cast<int64_t>(r.n) * p.H_kv >= p.tc_rows;
   }
-}
+  __device__ __forceinline__ int tiles_m(const SeqRows& r) const {
+    return static_cast<int>((static_cast<int64_t>(r.n) * p.H_kv + kRows - 1) / kRows);
+  }
+  __device__ __forceinline__ int tiles_k(const SeqRows& r) const {  // at least one
+    return max(1, ((r.pos + r.n - 1) / BK + BPT - 1) / BPT);
+  }
+  __device__ __forceinline__ int64_t count(const SeqRows& r) const {
+    return has(r) ? static_cast<int64_t>(tiles_m(r)) * ((tiles_k(r) + CT - 1) / CT) : 0;
+  }
+  __device__ __forceinline__ TcPlan(const ScoreParams& p_, int64_t* pre_) : p(p_), pre(pre_) {
+    const int code = blockIdx.x == 0 ? 202 : 0;
+    const int64_t visits = seq_scan(p.c.S, pre_, [&](int s) {
+      const SeqRows r = seq_rows(p, s, code);
+      return has(r) ? static_cast<int64_t>(tiles_m(r)) * tiles_k(r) : 0;
+    });
+    // eight units per SM, of at least 16 key tiles where there is that much work
+    const int64_t g = gridDim.x, one = (visits + g - 1) / g, eight = (visits + 8 * g - 1) / (8 * g);
+    CT = static_cast<int>(max(eight, min(one, static_cast<int64_t>(16))));
+    CT = max(CT, 1);
+    __syncthreads();
+    units = seq_scan(p.c.S, pre_, [&](int s) { return count(seq_rows(p, s, 0)); });
+  }
+  __device__ __forceinline__ TcUnit unit(int64_t u) const {
+    TcUnit it;
+    it.s = seq_find(p.c.S, pre, u, [&](int s) { return count(seq_rows(p, s, 0)); });
+    const SeqRows r = seq_rows(p, it.s, 0);
+    const int kt = tiles_k(r), nc = (kt + CT - 1) / CT;
+    const int m = static_cast<int>(u / nc), ch = static_cast<int>(u - static_cast<int64_t>(m) * nc);
+    it.first = m * kRows;
+    it.rows = min(kRows, r.n * p.H_kv - it.first);
+    it.row0 = static_cast<int64_t>(r.t0) * p.H_kv + it.first;
+    it.pos = r.pos;
+    it.own = (r.pos + (it.first + it.rows - 1) / p.H_kv) / BK;
+    it.k0 = ch * CT;
+    it.k1 = max(it.k0, min(it.k0 + CT, (it.own + BPT - 1) / BPT));
+    it.b_end = ch == nc - 1 ? p.c.max_pages : min((it.k0 + CT) * BPT, p.c.max_pages);
+    return it;
+  }
+};
 
 template <int D, int BK>
 __global__ void __launch_bounds__(kTcThreads, 1)
-    chunk_scores_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const TcParams p) {
+    chunk_scores_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const ScoreParams p) {
   using SH = TcShape<D, BK>;
   constexpr int ST = SH::ST, BPT = SH::BPT;
   extern __shared__ uint8_t smem_raw[];
@@ -305,7 +417,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   uint64_t* acc_empty = acc_full + 2;  // [2]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  const ChunkSeqs& c = p.s.c;
+  int64_t* pre = reinterpret_cast<int64_t*>(tmem_slot + 2);  // [threads + 1]
+  const ChunkSeqs& c = p.c;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -327,6 +440,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
+  const TcPlan<BK> plan(p, pre);
 
   if (warp == 0) {
     // -------------------------------------------------------- producer --
@@ -335,13 +449,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     if (lane == 0) prefetch_tmap(&tm_k);
     uint32_t g = 0;
     bool ok = true;
-    for (int u = blockIdx.x; ok && u < p.n_units; u += gridDim.x)
-      for_items<BK>(p, u, true, [&](const TcItem& it) {
+    for (int64_t u = blockIdx.x; ok && u < plan.units; u += gridDim.x) {
+        const TcUnit it = plan.unit(u);
         const int b0 = it.k0 * BPT, b1 = min(it.k1 * BPT, c.max_pages);
         auto fetch = [&](int b) {
           if (b >= b1) return -1;
           const int pg = static_cast<int>(chunk_page(c, it.s, b));
-          if (pg < 0 && b < it.own) report(p.s.status, DEV_ERR_BAD_INDEX, 201, it.s, b);
+          if (pg < 0 && b < it.own) report(p.status, DEV_ERR_BAD_INDEX, 201, it.s, b);
           return pg;
         };
         int mine = fetch(b0 + lane), next = fetch(b0 + 32 + lane);
@@ -358,7 +472,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             have |= pg[j] >= 0 ? 1 << j : 0;
           }
           const int st = g % ST;
-          ok = mbar_wait(&k_empty[st], ((g / ST) & 1) ^ 1, abort_flag, p.s.status, 200);
+          ok = mbar_wait(&k_empty[st], ((g / ST) & 1) ^ 1, abort_flag, p.status, 200);
           ok = __all_sync(0xFFFFFFFFu, ok);
           if (ok && lane == 0) {
             sOk[st] = have;
@@ -368,12 +482,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               if (pg[j] >= 0) {
                 const int row = pg[j] * BK;
                 tma_load_2d(sK + st * SH::K_BYTES + j * BK * D, &tm_k, &k_full[st], 0, row);
-                bulk_load(sS + st * kKeys + j * BK, p.s.scale + row, BK * 4, &k_full[st]);
+                bulk_load(sS + st * kKeys + j * BK, p.scale + row, BK * 4, &k_full[st]);
               }
           }
         }
-        return ok;
-      });
+    }
   } else if (warp == 1) {
     // ------------------------------------------------------------- MMA --
     if (lane == 0) {
@@ -383,16 +496,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const uint64_t k_desc = umma_desc(smem_u32(sK), 16, SH::SBO, SH::SWZ);
       uint32_t g = 0, ua = 0;
       bool ok = true;
-      for (int u = blockIdx.x; ok && u < p.n_units; u += gridDim.x, ++ua) {
+      for (int64_t u = blockIdx.x; ok && u < plan.units; u += gridDim.x, ++ua) {
         const int ab = ua & 1;
-        ok = mbar_wait(&a_full[ab], (ua >> 1) & 1, abort_flag, p.s.status, 210);
+        const TcUnit it = plan.unit(u);
+        ok = mbar_wait(&a_full[ab], (ua >> 1) & 1, abort_flag, p.status, 210);
         if (!ok) break;
         const uint64_t ad0 = a_desc + ab * (2 * SH::A_BYTES >> 4);
-        for_items<BK>(p, u, false, [&](const TcItem& it) {
           for (int kt = it.k0; ok && kt < it.k1; ++kt, ++g) {
             const int st = g % ST, acc = g & 1;
-            ok = mbar_wait(&k_full[st], (g / ST) & 1, abort_flag, p.s.status, 211) &&
-                 mbar_wait(&acc_empty[acc], ((g >> 1) & 1) ^ 1, abort_flag, p.s.status, 212);
+            ok = mbar_wait(&k_full[st], (g / ST) & 1, abort_flag, p.status, 211) &&
+                 mbar_wait(&acc_empty[acc], ((g >> 1) & 1) ^ 1, abort_flag, p.status, 212);
             if (!ok) break;
             tc_fence_after();
             const uint64_t kd = k_desc + st * (SH::K_BYTES >> 4);
@@ -408,13 +521,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             umma_commit(&k_empty[st]);
             umma_commit(&acc_full[acc]);
           }
-          return ok;
-        });
         umma_commit(&a_empty[ab]);
       }
       // the commits have arrived before the CTA ends
       for (uint32_t j = ua > 2 ? ua - 2 : 0; ok && j < ua; ++j)
-        ok = mbar_wait(&a_empty[j & 1], (j >> 1) & 1, abort_flag, p.s.status, 213);
+        ok = mbar_wait(&a_empty[j & 1], (j >> 1) & 1, abort_flag, p.status, 213);
     }
   } else if (warp >= 4 && warp < 8) {
     // ---------------------------------------------------------- queries --
@@ -422,18 +533,28 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     constexpr int LPR = D / 16, RPP = 128 / LPR;  // lanes per row, rows per pass
     const int tid = threadIdx.x - 128, l = tid % LPR;
     uint32_t ua = 0;
-    for (int u = blockIdx.x; u < p.n_units; u += gridDim.x, ++ua) {
+    for (int64_t u = blockIdx.x; u < plan.units; u += gridDim.x, ++ua) {
       const int ab = ua & 1;
-      if (!mbar_wait(&a_empty[ab], ((ua >> 1) & 1) ^ 1, abort_flag, p.s.status, 220)) break;
+      const TcUnit it = plan.unit(u);
+      if (!mbar_wait(&a_empty[ab], ((ua >> 1) & 1) ^ 1, abort_flag, p.status, 220)) break;
       uint8_t* hi = sA + ab * 2 * SH::A_BYTES;
-      const int64_t R0 = static_cast<int64_t>(u / p.nchunk) * kRows;
+      constexpr int NP = 4;  // passes whose rows are loaded together
 #pragma unroll 1
-      for (int r = tid / LPR; r < kRows; r += RPP) {
-        const bool on = R0 + r < p.rows;
-        const uint4* src = reinterpret_cast<const uint4*>(p.s.q + (R0 + (on ? r : 0)) * D) + 2 * l;
-        const uint4 raw[2] = {__ldg(src), __ldg(src + 1)};
+      for (int r0 = tid / LPR; r0 < kRows; r0 += NP * RPP) {
+        uint4 raw[NP][2];
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+          const int r = r0 + i * RPP;
+          const uint4* src =
+              reinterpret_cast<const uint4*>(p.q + (it.row0 + (r < it.rows ? r : 0)) * D) + 2 * l;
+          raw[i][0] = __ldg(src);
+          raw[i][1] = __ldg(src + 1);
+        }
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+        const int r = r0 + i * RPP;
         float x[16], amax = 0.f;
-        const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(raw);
+        const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(raw[i]);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const float2 f = __bfloat1622float2(h[e]);
@@ -472,7 +593,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         *reinterpret_cast<uint4*>(hi + r * D + chunk * 16) = make_uint4(ch[0], ch[1], ch[2], ch[3]);
         *reinterpret_cast<uint4*>(hi + SH::A_BYTES + r * D + chunk * 16) =
             make_uint4(cl[0], cl[1], cl[2], cl[3]);
-        if (l == 0) sRow[ab * kRows + r] = p.s.idx_scale * pow2(-shift);
+        if (l == 0) sRow[ab * kRows + r] = p.idx_scale * pow2(-shift);
+      }
       }
       fence_async_smem();
       __syncwarp();
@@ -484,21 +606,21 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const int tl = quarter * 32 + lane;  // TMEM lane; rows tl and tl + 128
     float* out_s = sOut + grp * kRows * SH::OUT;
     int* own_s = sOwn + grp * kRows;
-    const int H = p.s.H_kv, max_pages = c.max_pages;
+    const int H = p.H_kv, max_pages = c.max_pages;
     uint32_t g = 0, ua = 0;
     // after a wait that gave up, a warp goes the same way without waiting, so
     // that the group's barriers still meet
     bool ok = true;
-    for (int u = blockIdx.x; u < p.n_units; u += gridDim.x, ++ua) {
+    for (int64_t u = blockIdx.x; u < plan.units; u += gridDim.x, ++ua) {
       const int ab = ua & 1;
-      ok = ok && mbar_wait(&a_full[ab], (ua >> 1) & 1, abort_flag, p.s.status, 230);
+      const TcUnit it = plan.unit(u);
+      ok = ok && mbar_wait(&a_full[ab], (ua >> 1) & 1, abort_flag, p.status, 230);
       const float* row_f = sRow + ab * kRows;
-      const int R0 = u / p.nchunk * kRows;
-      const int b_end = min((u % p.nchunk + 1) * p.CT * BPT, max_pages);  // of this unit's blocks
-      for_items<BK>(p, u, false, [&](const TcItem& it) {
+      const int b_end = it.b_end;
+      float* out_g = p.out + it.row0 * max_pages;
         // the rows' own blocks, for the group's flushes
 #pragma unroll
-        for (int r = tl; r < kRows; r += 128) own_s[r] = (it.pos + (R0 + r) / H - it.ta) / BK;
+        for (int r = tl; r < kRows; r += 128) own_s[r] = (it.pos + (it.first + r) / H) / BK;
         int held = 0, kt_first = 0;  // tiles of this group that wait in out_s: kt_first, + 2, ...
         auto flush = [&] {
           constexpr int NV = kFlush * BPT;  // a row's values, one lane each
@@ -506,9 +628,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           const int v = tl % NV;
           const int b = (kt_first + 2 * (v / BPT)) * BPT + v % BPT;
           if (v < held * BPT && b < b_end) {
-            float* dst = p.s.out + static_cast<int64_t>(R0) * max_pages + b;
+            float* dst = out_g + b;
 #pragma unroll 4
-            for (int r = it.ra + tl / NV; r < it.rb; r += 128 / NV)
+            for (int r = tl / NV; r < it.rows; r += 128 / NV)
               dst[static_cast<int64_t>(r) * max_pages] =
                   b < own_s[r] ? out_s[r * SH::OUT + v] * row_f[r] : -INFINITY;
           }
@@ -518,8 +640,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         for (int kt = it.k0; kt < it.k1; ++kt, ++g) {
           if ((g & 1) != grp) continue;
           const int st = g % ST;
-          ok = ok && mbar_wait(&k_full[st], (g / ST) & 1, abort_flag, p.s.status, 231) &&
-               mbar_wait(&acc_full[grp], (g >> 1) & 1, abort_flag, p.s.status, 232);
+          ok = ok && mbar_wait(&k_full[st], (g / ST) & 1, abort_flag, p.status, 231) &&
+               mbar_wait(&acc_full[grp], (g >> 1) & 1, abort_flag, p.status, 232);
           ok = __all_sync(0xFFFFFFFFu, ok);
           tc_fence_after();
           const uint32_t ta = tmem_base + grp * 256 + (static_cast<uint32_t>(quarter * 32) << 16);
@@ -567,13 +689,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // blocks that no row of the item scores
         const int b0 = max(it.k0, it.k1) * BPT;
         if (b0 < b_end)
-          for (int r = it.ra + (warp - 8); r < it.rb; r += 8) {
-            float* dst = p.s.out + (static_cast<int64_t>(R0) + r) * max_pages;
+          for (int r = warp - 8; r < it.rows; r += 8) {
+            float* dst = out_g + static_cast<int64_t>(r) * max_pages;
             for (int b = b0 + lane; b < b_end; b += 32) dst[b] = -INFINITY;
           }
         asm volatile("bar.sync %0, 128;" ::"r"(1 + grp) : "memory");  // own_s is rewritten
-        return true;
-      });
       __syncwarp();
       if (lane == 0) mbar_arrive(&a_empty[ab]);
     }
@@ -675,11 +795,15 @@ __global__ void __launch_bounds__(256) block_topk_kernel(const TopkParams p) {
   else if (lane < p.k) dst[lane] = -1;
 }
 
-// Which form (see chunk_scores_tc_kernel).
-bool scores_on_tc(const ScoreLaunch& a) {
-  if (a.c.n_pages * a.c.B_k >= (int64_t(1) << 31)) return false;  // TMA row coordinates
-  return static_cast<int64_t>(a.c.T) * a.H_kv >= 256;
-}
+// A sequence's rows go to the tcgen05 kernel from this many on, each form taking
+// its own sequences of a batch, so that single tokens beside a long chunk cost
+// what they cost alone.  Rows in one sequence, mma.sync / tcgen05 in us:
+//            d_idx 64, 9K keys   61K keys     d_idx 128, 9K keys   61K keys
+//    256        10.3 / 16.6     16.5 / 18.6      12.4 / 21.0      24.0 / 24.7
+//    512        12.4 / 16.5     24.7 / 18.9      12.4 / 19.7      34.9 / 22.6
+//   1024        12.4 / 18.5     37.0 / 26.7      20.6 / 20.6      63.6 / 28.8
+//   2048        20.6 / 24.7     67.7 / 47.9      34.9 / 22.6     135.7 / 51.7
+constexpr int kTcRows = 512;
 
 template <int D, int BK>
 cudaError_t launch_scores_typed(const ScoreLaunch& a, cudaStream_t s) {
@@ -692,21 +816,13 @@ cudaError_t launch_scores_typed(const ScoreLaunch& a, cudaStream_t s) {
   p.H_kv = a.H_kv;
   p.idx_scale = a.idx_scale;
   p.status = a.status;
+  const int64_t rows = static_cast<int64_t>(a.c.T) * a.H_kv;
   const int sms = num_sms();
-  if (scores_on_tc(a)) {
+  // TMA row coordinates are 32 bits
+  const bool tc = rows >= kTcRows && a.c.n_pages * BK < (int64_t(1) << 31);
+  p.tc_rows = tc ? kTcRows : INT_MAX;
+  if (tc) {
     using SH = TcShape<D, BK>;
-    TcParams t{};
-    t.s = p;
-    t.rows = a.c.T * a.H_kv;
-    // about eight units per SM, of at least 16 key tiles, so that whole units
-    // even out over the SMs
-    const int m = (t.rows + kRows - 1) / kRows;
-    const int tiles = (a.c.max_pages + SH::BPT - 1) / SH::BPT;
-    const int want = (8 * sms + m - 1) / m;
-    t.CT = (tiles + want - 1) / want;
-    if (t.CT < 16) t.CT = 16;
-    t.nchunk = (tiles + t.CT - 1) / t.CT;
-    t.n_units = m * t.nchunk;
     CUtensorMap tk;
     // index keys as rows of D bytes (a map of 16-bit elements: only bytes move)
     const uint64_t dims[2] = {static_cast<uint64_t>(D) / 2, static_cast<uint64_t>(a.c.n_pages) * BK};
@@ -718,25 +834,25 @@ cudaError_t launch_scores_typed(const ScoreLaunch& a, cudaStream_t s) {
                                          static_cast<int>(SH::SMEM));
     if (e != cudaSuccess) return e;
     prof_begin("chunk_scores_tc", s);
-    chunk_scores_tc_kernel<D, BK><<<t.n_units < sms ? t.n_units : sms, kTcThreads, SH::SMEM, s>>>(tk, t);
+    chunk_scores_tc_kernel<D, BK><<<sms, kTcThreads, SH::SMEM, s>>>(tk, p);
     prof_end(s);
-    return cudaGetLastError();
+    e = cudaGetLastError();
+    // a single sequence of so many rows leaves the other form nothing
+    if (e != cudaSuccess || a.c.S == 1) return e;
   }
   // Columns per tile: 8 while there are no more tokens than sequences (single
-  // tokens share no keys), else 32.
-  const bool wide = a.c.T > a.c.S && a.c.T * a.H_kv > 8;
-  p.tpt = (wide ? 32 : 8) / a.H_kv;
-  const int tiles = (a.c.T + p.tpt - 1) / p.tpt;
-  // about four CTAs per SM over all tiles, and no more than the blocks need
-  int split = (4 * sms + tiles - 1) / tiles;
-  const int most = (a.c.max_pages + 7) / 8;
-  if (split > most) split = most;
-  const dim3 grid(split, tiles);
+  // tokens share no keys, and fewer registers let twice as many warps load), else
+  // up to 32.  The grid is what the SMs hold, fewer when tokens x blocks are.
+  const bool wide = a.c.T > a.c.S && rows > 8;
+  const int64_t most = static_cast<int64_t>(a.c.T) * ((a.c.max_pages + 7) / 8);
+  const int64_t held = (wide ? kHeld<D, 4> : kHeld<D, 1>) * sms;
+  const dim3 grid(static_cast<unsigned>(most < held ? most : held));
   prof_begin("chunk_scores", s);
-  if (wide) chunk_scores_kernel<D, BK, 4><<<grid, 256, 0, s>>>(p);
-  else chunk_scores_kernel<D, BK, 1><<<grid, 256, 0, s>>>(p);
+  const cudaError_t e =
+      wide ? launch_pdl(chunk_scores_kernel<D, BK, 4>, grid, dim3(256), 0, s, p)
+           : launch_pdl(chunk_scores_kernel<D, BK, 1>, grid, dim3(256), 0, s, p);
   prof_end(s);
-  return cudaGetLastError();
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace

@@ -445,8 +445,10 @@ MSA_API msa_status msa_paged_gather_fp8(const msa_chunk_dims* dims, const void* 
  *          (products that are NaN do not count); -inf for its own block, which
  *          Eq. 7 keeps without a score, for later ones, and for a block whose
  *          page is outside the pool
- * Dot products are exact to fp32 accumulation: bf16 queries and E4M3 codes
- * enter the tensor cores unrounded. */
+ * Dot products accumulate in fp32.  Codes and queries, which must be finite,
+ * enter the tensor cores unrounded, but that in sequences with many new rows
+ * the elements of a query below 2^-10 of its largest are rounded, by 2^-17 of
+ * that largest at most. */
 MSA_API msa_status msa_paged_index_scores_fp8(const msa_chunk_dims* dims, const void* q_idx,
                                               const void* kidx_pages, const float* kidx_scale,
                                               const int32_t* page_table, const int32_t* cu_new,
