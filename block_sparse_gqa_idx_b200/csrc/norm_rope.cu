@@ -7,13 +7,18 @@
 // Backward, with g = R(pos)^T dy:
 //   dw = sum over rows of g * n,  dx = (w g - n mean(w g n)) / sqrt(mean(x^2) + eps)
 //
-// A row (one head of one token) is read once by d/8 lanes, 16 bytes each, and
-// stays in registers: the mean is a shuffle reduction over those lanes and the
-// partner of a rotated pair is one shuffle away.  The angle never loses its
-// far positions: inv_freq is held as a fraction of a turn in 64-bit fixed
-// point, so pos * turn modulo 2^64 is the exact fractional turn, and
-// sincospi sees at most half a turn.  A token's cosines and sines are computed
-// once per CTA and shared by all of its heads.
+// Both are bound by the bytes of the rows.  A row (one head of one token) is
+// read once by d/8 lanes and stays in registers.  A lane holds four dimensions and
+// the four that they rotate with (rows' halves are read as 8-byte pieces, whole
+// 128-byte lines of a row together), so that turning needs no exchange and only
+// the sums are shuffle reductions.  A warp takes the rows of one token, several
+// loads in flight, and computes that token's cosines and sines itself while the
+// first rows are on their way: no barrier.  The angle never loses its far
+// positions: inv_freq is held as a fraction of a turn in 64-bit fixed point, so
+// pos * turn modulo 2^64 is the exact fractional turn, and sincospi sees at most
+// half a turn.
+// 32768 tokens of 32 + 4 heads of 128: 107 us forward (5.6 TB/s), 186 us
+// backward (4.9 TB/s, of it 11 for the weights' last sum).
 #include <math_constants.h>
 
 #include "msa_internal.h"
@@ -36,27 +41,27 @@ struct NRParams {
   uint64_t turn[64];          // inv_freq / (2 pi) in units of 2^-64 turns
 };
 
+// A lane's share of a row: dimensions d0 .. d0+3 and d1 .. d1+3.
 struct Row8 {
   float v[8];
 };
+struct Raw8 {
+  uint2 a, b;
+};
 
-__device__ __forceinline__ Row8 unpack8(uint4 u) {
+__device__ __forceinline__ Row8 unpack8(const Raw8& u) {
   Row8 r;
-  const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&u);
+  const uint32_t w[4] = {u.a.x, u.a.y, u.b.x, u.b.y};
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    const float2 f = __bfloat1622float2(h[e]);
+    const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[e]));
     r.v[2 * e] = f.x;
     r.v[2 * e + 1] = f.y;
   }
   return r;
 }
-__device__ __forceinline__ uint4 pack8(const Row8& r) {
-  return make_uint4(pack_bf16(r.v[0], r.v[1]), pack_bf16(r.v[2], r.v[3]),
-                    pack_bf16(r.v[4], r.v[5]), pack_bf16(r.v[6], r.v[7]));
-}
 
-// Sum over the LPR lanes that hold one row.
+// Sums over the LPR lanes that hold one row.
 template <int LPR>
 __device__ __forceinline__ float row_sum(float x) {
 #pragma unroll
@@ -64,110 +69,114 @@ __device__ __forceinline__ float row_sum(float x) {
   return x;
 }
 
-// This lane's cosines and sines.  Pairs (j, j + half): lane l holds
-// dimensions 8l .. 8l+7, which rotate with those of lane l -+ half/8; `sn` is
-// then the sine with the sign of this side.  Interleaved: four pairs in the
-// lane.  Dimensions that pass through get cos 1, sin 0.
+// Where a lane's dimensions are and the angles of its pairs: (d0 + e, d1 + e), or
+// the neighbours of d0 .. d0+7 when interleaved.  The first rot/8 lanes of a row
+// rotate; the others' dimensions follow behind rot and pass (cos 1, sin 0).
 template <int LPR, bool INTER>
-struct Angles {
-  float cs[INTER ? 4 : 8], sn[INTER ? 4 : 8];
-  int partner;  // lane (within the warp) of the paired dimensions
+struct Lane {
+  int d0, d1;
+  float cs[4], sn[4];
 
-  __device__ __forceinline__ void load(const float2* tab, int half, int lane) {
-    const int l = lane % LPR;
-    partner = lane;
-    if constexpr (INTER) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int j = 4 * l + e;
-        const float2 a = j < half ? tab[j] : make_float2(1.f, 0.f);
-        cs[e] = a.x;
-        sn[e] = a.y;
-      }
-    } else {
-      const int hl = half / 8;
-      const bool lo = l < hl, hi = !lo && l < 2 * hl;
-      if (lo) partner = lane + hl;
-      if (hi) partner = lane - hl;
-      const int j0 = lo ? 8 * l : (hi ? 8 * (l - hl) : 0);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float2 a = lo || hi ? tab[j0 + e] : make_float2(1.f, 0.f);
-        cs[e] = a.x;
-        sn[e] = lo ? -a.y : a.y;
-      }
+  __device__ __forceinline__ Lane(int half, int l) {
+    d0 = 8 * l;
+    d1 = d0 + 4;
+    if (!INTER && l < half / 4) {
+      d0 = 4 * l;
+      d1 = d0 + half;
     }
+  }
+  // The token's angles, by way of `tab` (the warp's own).
+  __device__ __forceinline__ void angles(const NRParams& p, int pos, float2* tab, int lane) {
+    for (int j = lane; j < p.half; j += 32) {
+      const uint64_t frac = static_cast<uint64_t>(static_cast<int64_t>(pos)) * p.turn[j];
+      float s, c;  // frac as a signed fraction of half a turn
+      sincospif(static_cast<float>(static_cast<int64_t>(frac)) * 0x1p-63f, &s, &c);
+      tab[j] = make_float2(c, s);
+    }
+    __syncwarp();
+    const int j0 = 4 * (lane % LPR);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 a = j0 < p.half ? tab[j0 + e] : make_float2(1.f, 0.f);
+      cs[e] = a.x;
+      sn[e] = a.y;
+    }
+    __syncwarp();
   }
   // y = R x (sgn = 1) or R^T x (sgn = -1)
   __device__ __forceinline__ Row8 turn(const Row8& x, float sgn) const {
     Row8 y;
-    if constexpr (INTER) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float a = x.v[2 * e], b = x.v[2 * e + 1], s = sgn * sn[e];
-        y.v[2 * e] = a * cs[e] - b * s;
-        y.v[2 * e + 1] = b * cs[e] + a * s;
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float other = __shfl_sync(0xFFFFFFFFu, x.v[e], partner);
-        y.v[e] = x.v[e] * cs[e] + other * (sgn * sn[e]);
-      }
+    for (int e = 0; e < 4; ++e) {
+      const int i = INTER ? 2 * e : e, j = INTER ? 2 * e + 1 : e + 4;
+      const float a = x.v[i], b = x.v[j], s = sgn * sn[e];
+      y.v[i] = a * cs[e] - b * s;
+      y.v[j] = b * cs[e] + a * s;
     }
     return y;
   }
+  template <int D>
+  __device__ __forceinline__ Raw8 load(const __nv_bfloat16* x, int64_t row) const {
+    const __nv_bfloat16* at = x + row * D;
+    return {__ldcs(reinterpret_cast<const uint2*>(at + d0)),
+            __ldcs(reinterpret_cast<const uint2*>(at + d1))};
+  }
+  __device__ __forceinline__ Row8 weight(const __nv_bfloat16* w) const {
+    Row8 r;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) r.v[e] = 1.f;
+    if (w != nullptr)
+      r = unpack8({__ldg(reinterpret_cast<const uint2*>(w + d0)),
+                   __ldg(reinterpret_cast<const uint2*>(w + d1))});
+    return r;
+  }
+  template <int D>
+  __device__ __forceinline__ void store(__nv_bfloat16* y, int64_t row, const Row8& r) const {
+    __nv_bfloat16* at = y + row * D;
+    *reinterpret_cast<uint2*>(at + d0) =
+        make_uint2(pack_bf16(r.v[0], r.v[1]), pack_bf16(r.v[2], r.v[3]));
+    *reinterpret_cast<uint2*>(at + d1) =
+        make_uint2(pack_bf16(r.v[4], r.v[5]), pack_bf16(r.v[6], r.v[7]));
+  }
 };
 
-// cos and sin of the `half` angles of each of the CTA's tokens, into smem.
-template <int TOK>
-__device__ __forceinline__ void fill_table(const NRParams& p, int t0, float2 (*tab)[64]) {
-  for (int i = threadIdx.x; i < TOK * p.half; i += kThreads) {
-    const int u = i / p.half, j = i - u * p.half;
-    if (t0 + u >= p.T) continue;
-    const uint64_t frac = static_cast<uint64_t>(static_cast<int64_t>(p.pos[t0 + u])) * p.turn[j];
-    float s, c;  // frac as a signed fraction of half a turn
-    sincospif(static_cast<float>(static_cast<int64_t>(frac)) * 0x1p-63f, &s, &c);
-    tab[u][j] = make_float2(c, s);
-  }
-}
-
-// TOK tokens per CTA, kWarps / TOK warps on each; a warp takes 32 / LPR rows
-// at a time.  Rows of a token with pos < 0 (padding) are left untouched.
+// TOK tokens per CTA, kWarps / TOK warps on each; a warp takes 32 / LPR rows at a
+// time.  Rows of a token with pos < 0 (padding) are left untouched.
 template <int D, bool INTER, int TOK>
 __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_constant__ NRParams p) {
   constexpr int LPR = D / 8, RPW = 32 / LPR, WPT = kWarps / TOK;
-  __shared__ float2 tab[TOK][64];
-  const int t0 = blockIdx.x * TOK;
-  fill_table<TOK>(p, t0, tab);
-  __syncthreads();
+  constexpr int U = TOK == 1 ? 1 : 4;  // loads in flight
+  constexpr int STEP = WPT * RPW;
+  __shared__ float2 tab[kWarps][64];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int u = warp / WPT, t = t0 + u;
-  if (t >= p.T || p.pos[t] < 0) return;
-  Angles<LPR, INTER> ang;
-  ang.load(tab[u], p.half, lane);
-  const int first = (warp % WPT) * RPW + lane / LPR, l = lane % LPR;
+  const int t = blockIdx.x * TOK + warp / WPT;
+  if (t >= p.T) return;
+  const int pos = __ldg(p.pos + t);
+  if (pos < 0) return;
+  Lane<LPR, INTER> ln(p.half, lane % LPR);
+  const int first = (warp % WPT) * RPW + lane / LPR;
+  bool have = false;
 #pragma unroll
   for (int which = 0; which < 2; ++which) {
     const int H = p.H[which];
-    Row8 w;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) w.v[e] = 1.f;
-    if (p.w[which] != nullptr) w = unpack8(reinterpret_cast<const uint4*>(p.w[which])[l]);
     const int64_t base = static_cast<int64_t>(t) * H;
-    const uint4* src = reinterpret_cast<const uint4*>(p.x[which]);
-    uint4* dst = reinterpret_cast<uint4*>(p.out[which]);
-    // two rows in flight per lane; whole warps stay in the loop (shuffles)
-    for (int h0 = 0; h0 < H; h0 += 2 * WPT * RPW) {
-      uint4 raw[2];
+    const Row8 w = ln.weight(p.w[which]);
+    // whole warps stay in the loop (shuffles)
+    for (int h0 = 0; h0 < H; h0 += U * STEP) {
+      Raw8 raw[U];
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        const int h = h0 + b * WPT * RPW + first;
-        raw[b] = h < H ? src[(base + h) * LPR + l] : make_uint4(0, 0, 0, 0);
+      for (int b = 0; b < U; ++b) {
+        const int h = h0 + b * STEP + first;
+        raw[b] = ln.template load<D>(p.x[which], base + (h < H ? h : 0));
+      }
+      if (!have) {
+        ln.angles(p, pos, tab[warp], lane);
+        have = true;
       }
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        const int h = h0 + b * WPT * RPW + first;
+      for (int b = 0; b < U; ++b) {
+        const int h = h0 + b * STEP + first;
+        if (h0 + b * STEP >= H) break;
         Row8 x = unpack8(raw[b]);
         float ss = 0.f;
 #pragma unroll
@@ -175,8 +184,8 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
         const float r = rsqrtf(row_sum<LPR>(ss) * (1.f / D) + p.eps);
 #pragma unroll
         for (int e = 0; e < 8; ++e) x.v[e] = x.v[e] * r * w.v[e];
-        const Row8 y = ang.turn(x, 1.f);
-        if (h < H) dst[(base + h) * LPR + l] = pack8(y);
+        const Row8 y = ln.turn(x, 1.f);
+        if (h < H) ln.template store<D>(p.out[which], base + h, y);
       }
     }
   }
@@ -187,27 +196,25 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
 // norm_rope_dw_kernel adds them in a fixed order (no atomics: the result does
 // not depend on timing).  Rows of padding tokens get zero gradients.
 template <int D, bool INTER, int TOK>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 3)
     norm_rope_bwd_kernel(const __grid_constant__ NRParams p) {
   constexpr int LPR = D / 8, RPW = 32 / LPR, WPT = kWarps / TOK;
-  __shared__ float2 tab[TOK][64];
+  constexpr int U = TOK == 1 ? 1 : 2;
+  constexpr int STEP = WPT * RPW;
+  __shared__ float2 tab[kWarps][64];
   __shared__ float red[kWarps * RPW][D];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int u = warp / WPT;
-  const int first = (warp % WPT) * RPW + lane / LPR, l = lane % LPR;
+  const int first = (warp % WPT) * RPW + lane / LPR;
+  Lane<LPR, INTER> ln(p.half, lane % LPR);
   float dw[2][8];
 #pragma unroll
   for (int which = 0; which < 2; ++which)
 #pragma unroll
     for (int e = 0; e < 8; ++e) dw[which][e] = 0.f;
 
-  for (int t0 = blockIdx.x * TOK; t0 < p.T; t0 += gridDim.x * TOK) {
-    __syncthreads();
-    fill_table<TOK>(p, t0, tab);
-    __syncthreads();
-    const int t = t0 + u;
-    if (t >= p.T) continue;
-    if (p.pos[t] < 0) {
+  for (int t = blockIdx.x * TOK + warp / WPT; t < p.T; t += gridDim.x * TOK) {
+    const int pos = __ldg(p.pos + t);
+    if (pos < 0) {
 #pragma unroll
       for (int which = 0; which < 2; ++which)
         for (int i = (warp % WPT) * 32 + lane; i < p.H[which] * LPR; i += WPT * 32)
@@ -215,40 +222,51 @@ __global__ void __launch_bounds__(kThreads)
               make_uint4(0, 0, 0, 0);
       continue;
     }
-    Angles<LPR, INTER> ang;
-    ang.load(tab[u], p.half, lane);
+    bool have = false;
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
       const int H = p.H[which];
-      Row8 w;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) w.v[e] = 1.f;
-      if (p.w[which] != nullptr) w = unpack8(reinterpret_cast<const uint4*>(p.w[which])[l]);
       const int64_t base = static_cast<int64_t>(t) * H;
-      for (int h0 = 0; h0 < H; h0 += WPT * RPW) {
-        const int h = h0 + first;
-        const bool on = h < H;
-        const int64_t at = (base + h) * LPR + l;
-        const uint4 xr = on ? reinterpret_cast<const uint4*>(p.x[which])[at] : make_uint4(0, 0, 0, 0);
-        const uint4 gr = on ? reinterpret_cast<const uint4*>(p.dy[which])[at] : make_uint4(0, 0, 0, 0);
-        Row8 x = unpack8(xr);
-        const Row8 g = ang.turn(unpack8(gr), -1.f);
-        float ss = 0.f;
+      const Row8 w = ln.weight(p.w[which]);
+      for (int h0 = 0; h0 < H; h0 += U * STEP) {
+        Raw8 xr[U], gr[U];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(x.v[e], x.v[e], ss);
-        const float r = rsqrtf(row_sum<LPR>(ss) * (1.f / D) + p.eps);
-        float dot = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          x.v[e] *= r;  // n
-          dot = fmaf(w.v[e] * g.v[e], x.v[e], dot);
-          dw[which][e] = fmaf(g.v[e], x.v[e], dw[which][e]);
+        for (int b = 0; b < U; ++b) {
+          const int h = h0 + b * STEP + first;
+          const int64_t row = base + (h < H ? h : 0);
+          xr[b] = ln.template load<D>(p.x[which], row);
+          gr[b] = ln.template load<D>(p.dy[which], row);
         }
-        const float mean = row_sum<LPR>(dot) * (1.f / D);
-        Row8 dx;
+        if (!have) {
+          ln.angles(p, pos, tab[warp], lane);
+          have = true;
+        }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) dx.v[e] = r * (w.v[e] * g.v[e] - x.v[e] * mean);
-        if (on) reinterpret_cast<uint4*>(p.out[which])[at] = pack8(dx);
+        for (int b = 0; b < U; ++b) {
+          const int h = h0 + b * STEP + first;
+          if (h0 + b * STEP >= H) break;
+          const bool on = h < H;
+          const Row8 x = unpack8(xr[b]);
+          Row8 g = ln.turn(unpack8(gr[b]), -1.f);
+          float ss = 0.f, dot = 0.f;  // of x, and of w g with x
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            ss = fmaf(x.v[e], x.v[e], ss);
+            dot = fmaf(w.v[e] * g.v[e], x.v[e], dot);
+          }
+          ss = row_sum<LPR>(ss);
+          dot = row_sum<LPR>(dot);
+          const float r = rsqrtf(ss * (1.f / D) + p.eps);
+          const float mean = dot * r * (1.f / D);
+          Row8 dx;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float n = x.v[e] * r;
+            if (on) dw[which][e] = fmaf(g.v[e], n, dw[which][e]);
+            dx.v[e] = r * (w.v[e] * g.v[e] - n * mean);
+          }
+          if (on) ln.template store<D>(p.out[which], base + h, dx);
+        }
       }
     }
   }
@@ -257,7 +275,8 @@ __global__ void __launch_bounds__(kThreads)
   for (int which = 0; which < 2; ++which) {
     __syncthreads();
 #pragma unroll
-    for (int e = 0; e < 8; ++e) red[warp * RPW + lane / LPR][8 * l + e] = dw[which][e];
+    for (int e = 0; e < 8; ++e)
+      red[warp * RPW + lane / LPR][(e < 4 ? ln.d0 : ln.d1 - 4) + e] = dw[which][e];
     __syncthreads();
     for (int d = threadIdx.x; d < D; d += kThreads) {
       float s = 0.f;
@@ -316,8 +335,7 @@ NRParams params_of(const NormRopeLaunch& a) {
 }
 
 // Tokens per CTA: one while the tokens do not fill the SMs several times over
-// (more warps on each token), else four (the cosines and sines of a token are
-// then shared by two warps instead of eight).
+// (eight warps on each), else eight.
 bool few_tokens(int T) { return T < 8 * num_sms(); }
 
 template <int D, bool INTER>
@@ -325,14 +343,14 @@ cudaError_t launch_fwd(const NormRopeLaunch& a, cudaStream_t s) {
   const NRParams p = params_of(a);
   prof_begin("norm_rope", s);
   if (few_tokens(a.T)) norm_rope_kernel<D, INTER, 1><<<a.T, kThreads, 0, s>>>(p);
-  else norm_rope_kernel<D, INTER, 4><<<(a.T + 3) / 4, kThreads, 0, s>>>(p);
+  else norm_rope_kernel<D, INTER, 8><<<(a.T + 7) / 8, kThreads, 0, s>>>(p);
   prof_end(s);
   return cudaGetLastError();
 }
 
 int bwd_grid(int T) {
-  const int tiles = few_tokens(T) ? T : (T + 3) / 4;
-  const int most = num_sms() * 4;
+  const int tiles = few_tokens(T) ? T : (T + 7) / 8;
+  const int most = num_sms() * 3;
   return tiles < most ? tiles : most;
 }
 
@@ -343,7 +361,7 @@ cudaError_t launch_bwd(const NormRopeLaunch& a, cudaStream_t s) {
   const int grid = bwd_grid(a.T);
   prof_begin("norm_rope_bwd", s);
   if (few_tokens(a.T)) norm_rope_bwd_kernel<D, INTER, 1><<<grid, kThreads, 0, s>>>(p);
-  else norm_rope_bwd_kernel<D, INTER, 4><<<grid, kThreads, 0, s>>>(p);
+  else norm_rope_bwd_kernel<D, INTER, 8><<<grid, kThreads, 0, s>>>(p);
   prof_end(s);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || p.part == nullptr) return e;
