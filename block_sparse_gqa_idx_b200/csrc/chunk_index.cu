@@ -729,16 +729,38 @@ __device__ __forceinline__ float warp_sort_desc(float x, int lane) {
   return x;
 }
 
+// A score and its block as one number: larger scores first, of equal ones the
+// lower block (-0 counts as 0).
+__device__ __forceinline__ uint64_t topk_key(float x, int block) {
+  const uint32_t u = __float_as_uint(x + 0.f);
+  const uint32_t o = u & 0x80000000u ? ~u : u | 0x80000000u;
+  return (static_cast<uint64_t>(o) << 32) | ~static_cast<uint32_t>(block);
+}
+__device__ __forceinline__ void topk_unkey(uint64_t key, float& x, int& block) {
+  const uint32_t o = static_cast<uint32_t>(key >> 32);
+  x = __uint_as_float(o & 0x80000000u ? o & 0x7FFFFFFFu : ~o);
+  block = static_cast<int>(~static_cast<uint32_t>(key));
+}
+
 // One warp per row.  The row's candidates (blocks before its own) are read
 // once, NR * 32 of them at a time in registers.  The (k-1)-th largest of the 32
 // lanes' maxima is a lower bound of the (k-1)-th largest candidate, so only
-// the few candidates at or above it (and above what is kept already) enter the
-// running list, which lane i holds the i-th best of; each entry costs a
-// ballot and a shift.  Candidates come in ascending block order and a later
-// one must be larger to pass an earlier one: ties keep the lower block.
-// Scores of -inf and NaN are never chosen.
+// the few candidates at or above it (and above what is kept already) can enter:
+// about 22 of 1024 at k = 16.  They are gathered (each lane's behind those of the
+// lanes before it) and ranked with the kept ones by counting the larger ones; lane
+// i then holds the i-th best.  More than kGather of them (many equal scores) enter
+// the list one after another instead, each by a ballot and a shift: in ascending
+// block order, and a later one must be larger to pass an earlier one, so that ties
+// keep the lower block here too.  Scores of -inf and NaN are never chosen.
+// The bound is instructions, about 800 a row of 1024 blocks (issue slots 68 % busy):
+// 16384 such rows (67 MB) take 22.9 us, 128 rows of 257 4.8.
+constexpr int kGather = 64;
+constexpr int kTopkWarps = 2;  // rows per CTA
+
 template <int NR>
-__global__ void __launch_bounds__(256) block_topk_kernel(const TopkParams p) {
+__global__ void __launch_bounds__(32 * kTopkWarps, 32 / kTopkWarps) block_topk_kernel(const TopkParams p) {
+  constexpr int kList = kGather + 32;  // candidates and kept ones
+  __shared__ alignas(16) uint64_t lists[kTopkWarps][kList + 32];
   griddep_wait();  // the scores may still be in flight
   const int lane = threadIdx.x & 31;
   const int64_t row = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
@@ -754,34 +776,98 @@ __global__ void __launch_bounds__(256) block_topk_kernel(const TopkParams p) {
   int li = -1;
   for (int base = 0; base < n && k1 > 0; base += NR * 32) {
     float x[NR], mx = -INFINITY;
+    const float* at = src + base + lane;
+    const int left = n - base - lane;
 #pragma unroll
-    for (int j = 0; j < NR; ++j) {
-      const int b = base + 32 * j + lane;
-      x[j] = b < n ? __ldg(src + b) : -INFINITY;
-    }
+    for (int j = 0; j < NR; ++j) x[j] = 32 * j < left ? __ldg(at + 32 * j) : -INFINITY;
 #pragma unroll
     for (int j = 0; j < NR; ++j) mx = fmaxf(mx, x[j]);
     const float floor_ = __shfl_sync(0xFFFFFFFFu, warp_sort_desc(mx, lane), k1 - 1);
     float worst = __shfl_sync(0xFFFFFFFFu, lv, k1 - 1);
+    // what enters is above this: not below floor_, and above worst
+    const float lim = floor_ > worst ? nextafterf(floor_, -INFINITY) : worst;
+    unsigned in = 0;  // bit j: candidate j of this lane enters
 #pragma unroll
+    for (int j = 0; j < NR; ++j)
+      if (x[j] > lim) in |= 1u << j;
+    const int mine = __popc(in);
+    int upto = mine;  // the candidates of this lane and the ones before
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+      if (lane >= o) upto += y;
+    }
+    const int count = __shfl_sync(0xFFFFFFFFu, upto, 31);
+    if (count <= kGather) {
+      uint64_t* list = lists[threadIdx.x >> 5];
+      const int held = __popc(__ballot_sync(0xFFFFFFFFu, lane < k1 && li >= 0));
+      __syncwarp();
+      float2* to = reinterpret_cast<float2*>(list) + upto - mine;
+      for (; in != 0; in &= in - 1) {  // few: read again rather than picked from registers
+        const int j = __ffs(in) - 1;
+        *to++ = make_float2(__ldg(at + 32 * j), __int_as_float(base + 32 * j + lane));
+      }
+      if (lane < held) reinterpret_cast<float2*>(list)[count + lane] = make_float2(lv, __int_as_float(li));
+      __syncwarp();
+      const int all = count + held;
+      uint64_t key[kList / 32];
+      int rank[kList / 32];
+#pragma unroll
+      for (int c = 0; c < kList / 32; ++c) {
+        rank[c] = 0;
+        if (c * 32 + lane < all) {
+          const float2 e = reinterpret_cast<const float2*>(list)[c * 32 + lane];
+          key[c] = topk_key(e.x, __float_as_int(e.y));
+          list[c * 32 + lane] = key[c];
+        }
+      }
+      __syncwarp();
+      if (all <= 32) {
+        // two at a time; behind the last one key 0, which is larger than none
+        if (lane == 0) list[all] = 0;
+        __syncwarp();
+#pragma unroll 4
+        for (int j = 0; j < all; j += 2) {
+          const ulonglong2 two = *reinterpret_cast<const ulonglong2*>(list + j);
+          rank[0] += two.x > key[0] ? 1 : 0;
+          rank[0] += two.y > key[0] ? 1 : 0;
+        }
+      } else {
+        for (int j = 0; j < all; ++j) {
+          const uint64_t other = list[j];
+#pragma unroll
+          for (int c = 0; c < kList / 32; ++c) rank[c] += other > key[c] ? 1 : 0;
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < kList / 32; ++c)
+        if (c * 32 + lane < all && rank[c] < 32) list[kList + rank[c]] = key[c];
+      __syncwarp();
+      lv = -INFINITY;
+      li = -1;
+      if (lane < min(all, k1)) topk_unkey(list[kList + lane], lv, li);
+      continue;
+    }
+#pragma unroll 1
     for (int j = 0; j < NR; ++j) {
-      unsigned todo = __ballot_sync(0xFFFFFFFFu, x[j] > worst && x[j] >= floor_);
+      const float xj = 32 * j < left ? __ldg(at + 32 * j) : -INFINITY;
+      unsigned todo = __ballot_sync(0xFFFFFFFFu, xj > worst && xj > lim);
       while (todo != 0) {
         const int from = __ffs(todo) - 1;
-        const float v = __shfl_sync(0xFFFFFFFFu, x[j], from);
-        const int at = __popc(__ballot_sync(0xFFFFFFFFu, lv >= v));
+        const float v = __shfl_sync(0xFFFFFFFFu, xj, from);
+        const int to = __popc(__ballot_sync(0xFFFFFFFFu, lv >= v));
         const float uv = __shfl_up_sync(0xFFFFFFFFu, lv, 1);
         const int ui = __shfl_up_sync(0xFFFFFFFFu, li, 1);
-        if (lane > at) {
+        if (lane > to) {
           lv = uv;
           li = ui;
-        } else if (lane == at) {
+        } else if (lane == to) {
           lv = v;
           li = base + 32 * j + from;
         }
         worst = __shfl_sync(0xFFFFFFFFu, lv, k1 - 1);
         todo &= todo - 1;
-        todo &= __ballot_sync(0xFFFFFFFFu, x[j] > worst);
+        todo &= __ballot_sync(0xFFFFFFFFu, xj > worst);
       }
     }
   }
@@ -867,10 +953,10 @@ cudaError_t launch_block_topk(const float* scores, const int32_t* pos, int32_t* 
                               int H_kv, int n, int B_k, int k, cudaStream_t s) {
   const TopkParams p{scores, pos, idx, T, H_kv, n, B_k, k};
   const int64_t threads = static_cast<int64_t>(T) * H_kv * 32;
-  const dim3 grid(static_cast<unsigned>((threads + 255) / 256));
+  const dim3 block(32 * kTopkWarps), grid(static_cast<unsigned>((threads + block.x - 1) / block.x));
   prof_begin("block_topk", s);
-  const cudaError_t e = n <= 256 ? launch_pdl(block_topk_kernel<8>, grid, dim3(256), 0, s, p)
-                                 : launch_pdl(block_topk_kernel<32>, grid, dim3(256), 0, s, p);
+  const cudaError_t e = n <= 256 ? launch_pdl(block_topk_kernel<8>, grid, block, 0, s, p)
+                                 : launch_pdl(block_topk_kernel<32>, grid, block, 0, s, p);
   prof_end(s);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
