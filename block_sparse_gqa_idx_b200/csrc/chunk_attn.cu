@@ -252,8 +252,10 @@ struct Attend {
   }
 };
 
+template <int D, int NH>
+constexpr int kHeld = D == 128 ? (NH == 1 ? 3 : 2) : (NH == 1 ? 4 : 3);  // CTAs per SM
 template <int D, int BK, int NH>
-__global__ void __launch_bounds__(kWarps * 32) chunk_attend_kernel(const AttendParams p) {
+__global__ void __launch_bounds__(kWarps * 32, kHeld<D, NH>) chunk_attend_kernel(const AttendParams p) {
   using A = Attend<D, BK, NH>;
   constexpr int HEADS = 8 * NH;
   constexpr int GPB = BK / 16;  // 16-key groups per block
@@ -417,14 +419,27 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(const AttendParams p) {
     p.lse[w] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.6931471805599453f;
 }
 
-// Splits of a row's keys: enough CTAs for three per SM, at least one 16-key
-// group for every warp.
-int splits_of(int T, int H_kv, int B_k, int k) {
+// Splits of a row's keys: what ends first when a round of CTAs (as many as the SMs
+// hold) takes a warp's share of the 16-key groups and about four groups' time to
+// begin with, and a join costs as much again.  At least one group for every warp.
+// 48 rows of four groups, k = 16, B_k = 128, on 148 SMs: two splits 35 us, three
+// (a round and a third) 44, four 40, six 44.
+int splits_of(int T, int H_q, int H_kv, int B_k, int d_h, int k) {
   const int64_t units = static_cast<int64_t>(T) * H_kv;
-  int64_t n = (3 * static_cast<int64_t>(num_sms()) + units - 1) / units;
-  const int most = k * B_k / 16 / kWarps;
-  if (n > most) n = most;
-  return static_cast<int>(n > 32 ? 32 : n);
+  const int64_t held = static_cast<int64_t>(num_sms()) *
+                       (H_q / H_kv <= 8 ? (d_h == 128 ? kHeld<128, 1> : kHeld<64, 1>)
+                                        : (d_h == 128 ? kHeld<128, 2> : kHeld<64, 2>));
+  const int steps = k * B_k / 16 / kWarps;
+  int best = 1;
+  int64_t cost = 0;
+  for (int n = 1; n <= 32 && n <= steps; ++n) {
+    const int64_t c = (units * n + held - 1) / held * ((steps + n - 1) / n + 4) + (n > 1 ? 4 : 0);
+    if (n == 1 || c < cost) {
+      best = n;
+      cost = c;
+    }
+  }
+  return best;
 }
 
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
@@ -445,7 +460,7 @@ cudaError_t launch_direct(const AttendLaunch& a, cudaStream_t s) {
   p.H_kv = a.H_kv;
   p.G = a.H_q / a.H_kv;
   p.k = a.k;
-  p.nsplit = splits_of(a.c.T, a.H_kv, a.c.B_k, a.k);
+  p.nsplit = splits_of(a.c.T, a.H_q, a.H_kv, a.c.B_k, D, a.k);
   p.scale_log2 = a.scale * 1.4426950408889634f;
   p.status = a.status;
   const int64_t units = static_cast<int64_t>(a.c.T) * a.H_kv;
@@ -488,7 +503,7 @@ size_t chunk_attend_workspace_bytes(const ChunkSeqs& c, int H_q, int H_kv, int d
   if (c.T == 0) return 0;
   if (kv_outer(c, H_q, H_kv, d_h, k))
     return chunk_attend_kv_workspace_bytes(c.T, c.S, c.max_pages, H_q, H_kv, d_h, k);
-  const int n = splits_of(c.T, H_kv, c.B_k, k);
+  const int n = splits_of(c.T, H_q, H_kv, c.B_k, d_h, k);
   if (n == 1) return 0;
   const size_t rows = static_cast<size_t>(c.T) * H_q * n;
   return align256(sizeof(float) * rows * d_h) + align256(sizeof(float) * rows);
