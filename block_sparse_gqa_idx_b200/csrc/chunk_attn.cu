@@ -5,11 +5,15 @@
 //   S = (q e4m3(k_j)) ks_j scale,  O = sum_j softmax(S)_j vs_j e4m3(v_j)
 //
 // Query-outer kernel: one CTA per (row, group, split of the row's keys), four
-// warps that walk the row's 16-key groups independently; no shared memory and
-// no barrier until the warps' states are joined at the end.
-//   * Codes go from global memory into MMA fragments in registers, widened to
-//     f16 there (exact), so the tensor cores see the raw codes; a key's scale
-//     multiplies its scores, a value's scale its weight.
+// warps that walk the row's 16-key groups independently; no barrier until the
+// warps' states are joined at the end.
+//   * Each warp has its own ring of 16-key stages in shared memory, filled by
+//     asynchronous copies two stages ahead.  (Four and five stages, and four CTAs
+//     per SM, are slower, 34, 37 and 34 us against 32 in the case below: more reads
+//     of 128 bytes in flight do not help the memory.)
+//   * Codes go from there into MMA fragments, widened to f16 in registers (exact),
+//     so the tensor cores see the raw codes; a key's scale multiplies its scores, a
+//     value's scale its weight.
 //   * Both products are transposed so that the 16-row side of the MMA is keys
 //     (S^T = K Q^T) or dimensions (O^T = V^T P^T) and the 8-column side the
 //     group's heads: no row is padding at G = 8.  V^T pairs keys: two keys'
@@ -21,7 +25,8 @@
 //     (ref_y), apart from the softmax's own maximum (ref_x): P fits f16 for
 //     any value scales.  Both references move only when a score passes them
 //     by more than 2^10, so a step costs one vote instead of two reductions.
-//   * The loads of the next 16 keys are in flight while these are computed.
+// Single tokens of 48 sequences at 16K (H_q = 32, H_kv = 4, d_h = B_k = 128, k = 16;
+// 104 MB): 28 us, and 4 for the join of two splits; 3.7 TB/s.
 #include <cuda_fp8.h>
 
 #include "chunk_launch.h"
@@ -30,6 +35,7 @@ namespace msa {
 namespace {
 
 constexpr int kWarps = 4;
+constexpr int kStages = 3;
 constexpr float kSlack = 10.f;  // log2 of how far a weight may pass its reference
 
 struct AttendParams {
@@ -58,6 +64,12 @@ __device__ __forceinline__ uint32_t widen2(uint32_t c2) {
 __device__ __forceinline__ uint32_t pack_f16(float a, float b) {
   const __half2 h = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ void copy16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy4(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
 // 8x8 b16 transpose across the warp (row lane/4, columns 2 (lane%4), +1).
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
@@ -89,7 +101,9 @@ struct Attend {
   uint32_t bq[NH][NK][2];
   float un[NH][2];             // scale of the raw dots of heads 2t, 2t + 1 (log2 domain)
   float o[NH][MT][4];
-  float l[NH][2], rx[NH][2], ry[NH][2];
+  // sums; the references of scores and of weights (0 before the first key), and
+  // what a score or weight must pass for them to move
+  float l[NH][2], rx[NH][2], ry[NH][2], tx[NH][2], ty[NH][2];
 
   __device__ __forceinline__ void load_q(const AttendParams& p, int64_t row, int r, int lane) {
     const int g = lane >> 2, t = lane & 3;
@@ -124,43 +138,78 @@ struct Attend {
         const int sh = __shfl_sync(0xFFFFFFFFu, shift, (2 * t + e) * 4);
         un[n][e] = p.scale_log2 * pow2(-sh);
         l[n][e] = 0.f;
-        rx[n][e] = ry[n][e] = -INFINITY;
+        rx[n][e] = ry[n][e] = 0.f;
+        tx[n][e] = ty[n][e] = -INFINITY;
       }
 #pragma unroll
       for (int i = 0; i < MT; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.f;
     }
   }
 
-  __device__ __forceinline__ void load(const AttendParams& p, Raw& x, int64_t pg, int b, int key0,
-                                       int r, int lane) const {
+  // A stage: 16 keys' K rows, V rows, K scales, V scales.  16-byte chunks of a row
+  // are permuted so that a fragment load meets no bank twice.
+  static constexpr int STAGE = 32 * D + 128;
+  static __device__ __forceinline__ int chunk(int key, int c) {
+    return key * D + 16 * (D == 128 ? c ^ (key & 7) : c ^ ((key >> 1) & 3));
+  }
+  // What a lane copies of every stage, from the stage's first row on.
+  struct Share {
+    int dst[2];     // in the stage: the copies' two permutations
+    int64_t src;    // byte of the first copy
+    int64_t rows;   // bytes from a copy to the next
+    int64_t scale;  // element
+  };
+  static constexpr int C = D / 16;  // chunks per row
+  static __device__ __forceinline__ Share share(const AttendParams& p, int lane) {
+    const int key = lane / C, c = lane % C;
+    const int64_t row = static_cast<int64_t>(p.H_kv) * D;
+    Share h;
+    h.dst[0] = chunk(key, c);
+    h.dst[1] = chunk(key + 32 / C, c) - D * 32 / C;
+    h.src = key * row + 16 * c;
+    h.rows = row * (32 / C);
+    h.scale = static_cast<int64_t>(lane & 15) * p.H_kv;
+    return h;
+  }
+  static __device__ __forceinline__ void fill(const AttendParams& p, const Share& h, uint8_t* st,
+                                              int64_t row0, int lane) {
+    const int64_t at = row0 * D + h.src;
+#pragma unroll
+    for (int i = 0; i < C / 2; ++i) {
+      uint8_t* dst = st + h.dst[i & 1] + i * (D * 32 / C);
+      copy16(dst, p.kp + (at + i * h.rows));
+      copy16(dst + 16 * D, p.vp + (at + i * h.rows));
+    }
+    copy4(st + 32 * D + 4 * lane, (lane < 16 ? p.ks : p.vs) + (row0 + h.scale));
+  }
+  static __device__ __forceinline__ void load(Raw& x, const uint8_t* st, int j0, int lane) {
     const int g = lane >> 2, t = lane & 3;
-    const int64_t row0 = (pg * BK + key0) * p.H_kv + r;
+    const float* sc = reinterpret_cast<const float*>(st + 32 * D);
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const int64_t row = row0 + static_cast<int64_t>(g + 8 * e) * p.H_kv;
 #pragma unroll
       for (int u = 0; u < NU; ++u)
-        x.k[e][u] = __ldg(reinterpret_cast<const uint4*>(p.kp + row * D + t * DT) + u);
-      x.ks[e] = __ldg(p.ks + row);
-      x.vs[e] = __ldg(p.vs + row);
+        x.k[e][u] = *reinterpret_cast<const uint4*>(st + chunk(g + 8 * e, t * NU + u));
+      x.ks[e] = sc[g + 8 * e];
+      x.vs[e] = sc[16 + g + 8 * e];
     }
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const int64_t row = row0 + static_cast<int64_t>(2 * t + (e & 1) + 8 * (e >> 1)) * p.H_kv;
-      const uint8_t* src = p.vp + row * D + g * VB;
+      const int key = 2 * t + (e & 1) + 8 * (e >> 1);
+      const uint8_t* src = st + 16 * D + chunk(key, g * VB / 16) + g * VB % 16;
       if constexpr (VW == 4) {
-        const uint4 w = __ldg(reinterpret_cast<const uint4*>(src));
+        const uint4 w = *reinterpret_cast<const uint4*>(src);
         x.v[e][0] = w.x;
         x.v[e][1] = w.y;
         x.v[e][2] = w.z;
         x.v[e][3] = w.w;
       } else {
-        const uint2 w = __ldg(reinterpret_cast<const uint2*>(src));
+        const uint2 w = *reinterpret_cast<const uint2*>(src);
         x.v[e][0] = w.x;
         x.v[e][1] = w.y;
       }
     }
-    x.j0 = b * BK + key0;
+    x.j0 = j0;
   }
 
   __device__ __forceinline__ void step(Raw& x, int pos, int lane) {
@@ -199,21 +248,26 @@ struct Attend {
     for (int n = 0; n < NH; ++n)
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        pass = pass || s[n][e] > rx[n][e & 1] + kSlack || y[n][e] > ry[n][e & 1] + kSlack;
+        pass = pass || s[n][e] > tx[n][e & 1] || y[n][e] > ty[n][e & 1];
     if (__any_sync(0xFFFFFFFFu, pass)) {
 #pragma unroll
       for (int n = 0; n < NH; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float mx = fmax3(rx[n][e], s[n][e], s[n][e + 2]);
-          float my = fmax3(ry[n][e], y[n][e], y[n][e + 2]);
+          float mx = fmax3(tx[n][e] - kSlack, s[n][e], s[n][e + 2]);
+          float my = fmax3(ty[n][e] - kSlack, y[n][e], y[n][e + 2]);
 #pragma unroll
           for (int w = 4; w < 32; w <<= 1) {
             mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, w));
             my = fmaxf(my, __shfl_xor_sync(0xFFFFFFFFu, my, w));
           }
-          l[n][e] *= exp2f(rel(rx[n][e], mx));
-          const float f = exp2f(rel(ry[n][e], my));
+          tx[n][e] = mx + kSlack;
+          ty[n][e] = my + kSlack;
+          mx = mx == -INFINITY ? 0.f : mx;
+          my = my == -INFINITY ? 0.f : my;
+          // (nothing is in the sums before the first key, whatever the factor)
+          l[n][e] *= exp2f(fminf(rx[n][e] - mx, 0.f));
+          const float f = exp2f(fminf(ry[n][e] - my, 0.f));
 #pragma unroll
           for (int i = 0; i < MT; ++i) {
             o[n][i][e] *= f;
@@ -229,8 +283,8 @@ struct Attend {
       float w[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        l[n][e & 1] += ex2_ftz(rel(s[n][e], rx[n][e & 1]));
-        w[e] = copysignf(ex2_ftz(rel(y[n][e], ry[n][e & 1])), x.vs[e >> 1]);
+        l[n][e & 1] += ex2_ftz(s[n][e] - rx[n][e & 1]);
+        w[e] = copysignf(ex2_ftz(y[n][e] - ry[n][e & 1]), x.vs[e >> 1]);
       }
       pb[n][0] = transpose8(pack_f16(w[0], w[1]));
       pb[n][1] = transpose8(pack_f16(w[2], w[3]));
@@ -259,10 +313,11 @@ __global__ void __launch_bounds__(kWarps * 32, kHeld<D, NH>) chunk_attend_kernel
   using A = Attend<D, BK, NH>;
   constexpr int HEADS = 8 * NH;
   constexpr int GPB = BK / 16;  // 16-key groups per block
-  __shared__ float so[kWarps][HEADS][D];
+  extern __shared__ __align__(128) uint8_t smem[];
+  float (*so)[HEADS][D] = reinterpret_cast<float (*)[HEADS][D]>(smem);  // once the rings are done
   __shared__ float sl[kWarps][HEADS], sx[kWarps][HEADS], sy[kWarps][HEADS];
   __shared__ int2 slots[32];  // (page, block) of the row's usable slots
-  __shared__ int n_slots;
+  __shared__ int n_full, n_own;  // other blocks, and the own one as often as it is listed
 
   const int sp = blockIdx.x % p.nsplit;
   const int64_t unit = blockIdx.x / p.nsplit;  // (row, group)
@@ -285,35 +340,63 @@ __global__ void __launch_bounds__(kWarps * 32, kHeld<D, NH>) chunk_attend_kernel
       pg = chunk_page(p.c, tok.s, b);
       if (pg < 0) report(p.status, DEV_ERR_BAD_INDEX, 132, tok.s, b);
     }
-    const unsigned use = __ballot_sync(0xFFFFFFFFu, pg >= 0);
-    if (pg >= 0) slots[__popc(use & ((1u << lane) - 1))] = make_int2(static_cast<int>(pg), b);
-    if (lane == 0) n_slots = __popc(use);
+    // the row's own block behind the others: the keys after the row are its last
+    const bool last = pg >= 0 && b == tok.pos / BK;
+    const unsigned use = __ballot_sync(0xFFFFFFFFu, pg >= 0 && !last);
+    const unsigned end = __ballot_sync(0xFFFFFFFFu, last);
+    const unsigned before = (1u << lane) - 1;
+    if (pg >= 0)
+      slots[last ? __popc(use) + __popc(end & before) : __popc(use & before)] =
+          make_int2(static_cast<int>(pg), b);
+    if (lane == 0) {
+      n_full = __popc(use);
+      n_own = __popc(end);
+    }
   }
   A a;
   a.load_q(p, row, r, lane);
   __syncthreads();
-  const int total = n_slots * GPB;
+  const int full = n_full * GPB, own = (tok.pos % BK) / 16 + 1;  // groups with keys of the row
+  const int total = full + n_own * own;
   const int stride = p.nsplit * kWarps;
-  // the next group from i on that holds a key of this row
-  auto seek = [&](int i) {
-    while (i < total && slots[i / GPB].y * BK + (i % GPB) * 16 > tok.pos) i += stride;
-    return i;
+  uint8_t* ring = smem + warp * kStages * A::STAGE;
+  const typename A::Share mine = A::share(p, lane);
+  int ahead = sp * kWarps + warp;
+  int j0[kStages - 1];  // first keys of the groups on their way
+  auto fetch = [&](int stage) {
+    int first = 0;
+    if (ahead < total) {
+      int slot = ahead / GPB, group = ahead % GPB;
+      if (ahead >= full) {
+        slot = (ahead - full) / own;
+        group = ahead - full - slot * own;
+        slot += n_full;
+      }
+      const int2 block = slots[slot];
+      const int64_t key = static_cast<int64_t>(block.x) * BK + group * 16;
+      A::fill(p, mine, ring + stage * A::STAGE, key * p.H_kv + r, lane);
+      first = block.y * BK + group * 16;
+    }
+    ahead += stride;
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    return first;
   };
-  auto fetch = [&](typename A::Raw& x, int i) {
-    if (i < total) a.load(p, x, slots[i / GPB].x, slots[i / GPB].y, (i % GPB) * 16, r, lane);
-  };
-  typename A::Raw x0, x1;
-  int i = seek(sp * kWarps + warp);
-  fetch(x0, i);
-  while (i < total) {
-    const int i1 = seek(i + stride);
-    fetch(x1, i1);
-    a.step(x0, tok.pos, lane);
-    if (i1 >= total) break;
-    i = seek(i1 + stride);
-    fetch(x0, i);
-    a.step(x1, tok.pos, lane);
+#pragma unroll
+  for (int s = 0; s < kStages - 1; ++s) j0[s] = fetch(s);
+  int stage = 0;
+  for (int i = sp * kWarps + warp; i < total; i += stride) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+    __syncwarp();  // and all lanes have read the stage that is filled next
+    const int now = j0[0];
+#pragma unroll
+    for (int s = 0; s + 2 < kStages; ++s) j0[s] = j0[s + 1];
+    j0[kStages - 2] = fetch(stage == 0 ? kStages - 1 : stage - 1);
+    typename A::Raw x;
+    A::load(x, ring + stage * A::STAGE, now, lane);
+    a.step(x, tok.pos, lane);
+    stage = stage + 1 == kStages ? 0 : stage + 1;
   }
+  __syncthreads();
 
   // join the four warps' states
   const int g = lane >> 2, t = lane & 3;
@@ -327,8 +410,8 @@ __global__ void __launch_bounds__(kWarps * 32, kHeld<D, NH>) chunk_attend_kernel
       for (int w = 4; w < 32; w <<= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, w);
       if (g == 0) {
         sl[warp][h] = l;
-        sx[warp][h] = a.rx[n][e];
-        sy[warp][h] = a.ry[n][e];
+        sx[warp][h] = a.tx[n][e] == -INFINITY ? -INFINITY : a.rx[n][e];
+        sy[warp][h] = a.ty[n][e] == -INFINITY ? -INFINITY : a.ry[n][e];
       }
 #pragma unroll
       for (int m = 0; m < A::MT; ++m)
@@ -444,6 +527,18 @@ int splits_of(int T, int H_q, int H_kv, int B_k, int d_h, int k) {
 
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
+template <int D, int BK, int NH>
+cudaError_t launch_attend(const AttendParams& p, unsigned grid, cudaStream_t s) {
+  constexpr int ring = kWarps * kStages * Attend<D, BK, NH>::STAGE;
+  static_assert(ring >= kWarps * 8 * NH * D * 4 && kHeld<D, NH> * (ring + 2048) <= 227 * 1024,
+                "the states to join, and the CTAs an SM holds");
+  const cudaError_t e = cudaFuncSetAttribute(chunk_attend_kernel<D, BK, NH>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, ring);
+  if (e != cudaSuccess) return e;
+  chunk_attend_kernel<D, BK, NH><<<grid, kWarps * 32, ring, s>>>(p);
+  return cudaGetLastError();
+}
+
 template <int D, int BK>
 cudaError_t launch_direct(const AttendLaunch& a, cudaStream_t s) {
   AttendParams p{};
@@ -469,10 +564,8 @@ cudaError_t launch_direct(const AttendLaunch& a, cudaStream_t s) {
       static_cast<uint8_t*>(a.ws) + align256(sizeof(float) * units * p.nsplit * p.G * D));
   const unsigned grid = static_cast<unsigned>(units * p.nsplit);
   prof_begin("chunk_attend", s);
-  if (p.G <= 8) chunk_attend_kernel<D, BK, 1><<<grid, kWarps * 32, 0, s>>>(p);
-  else chunk_attend_kernel<D, BK, 2><<<grid, kWarps * 32, 0, s>>>(p);
+  cudaError_t e = p.G <= 8 ? launch_attend<D, BK, 1>(p, grid, s) : launch_attend<D, BK, 2>(p, grid, s);
   prof_end(s);
-  cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || p.nsplit == 1) return e;
   const int64_t threads = static_cast<int64_t>(a.c.T) * a.H_q * 32;
   prof_begin("chunk_join", s);
