@@ -577,19 +577,20 @@ cudaError_t launch_direct(const AttendLaunch& a, cudaStream_t s) {
 
 }  // namespace
 
-// Which form.  The query-outer kernel's time is the bytes of the selected
-// pages as every row reads them (through L2); the KV-outer form costs about 30
-// us of short kernels and each page once, and pays from about 2^27 such values
-// on (H_q = 32, H_kv = 4, d_h = B_k = 128, k = 16: 128 rows).  Measured there,
-// query-outer against KV-outer, one sequence at 9K / at 61K: 64 rows 46 : 39 /
-// 50 : 83 us, 128 rows 68 : 47 / 76 : 90, 256 rows 106 : 56 / 114 : 93, 512 rows
-// 184 : 81 / 193 : 137; at d_h = B_k = 64, k = 8, 512 rows 43 : 43 / 45 : 88.
+// Which form.  The query-outer kernel's time is the bytes of the selected pages as
+// every row reads them (through L2); the KV-outer form costs about 30 us of short
+// kernels and each page once, and pays from about 2^28 such values on (H_q = 32,
+// H_kv = 4, d_h = B_k = 128, k = 16: 256 rows).  Measured there, query-outer against
+// KV-outer, one sequence at 9K / four at 9K / one at 61K: 128 rows 53 : 47 / 53 : 62 /
+// 54 : 90 us, 256 rows 92 : 57 / 93 : 82 / 94 : 92, 512 rows 150 : 82 / 152 : 112 /
+// 152 : 137; H_q = 8, H_kv = 2, 256 rows 51 : 40 / 52 : 50 / 51 : 55; d_h = B_k = 64,
+// k = 8, 512 rows 39 : 44 / 39 : 59 / 39 : 91.
 static bool kv_outer(const msa::ChunkSeqs& c, int H_q, int H_kv, int d_h, int k) {
   const int G = H_q / H_kv;
   if (16 % G != 0 || (G < 8 && H_q % 8 != 0)) return false;  // its MMA rows and TMA boxes
   if (static_cast<int64_t>(c.S) * c.max_pages * H_kv >= (int64_t(1) << 30)) return false;  // keys
   if (c.n_pages * c.B_k >= (int64_t(1) << 31)) return false;  // TMA row coordinates
-  return static_cast<int64_t>(c.T) * H_kv * k * c.B_k * d_h >= (int64_t(1) << 27);
+  return static_cast<int64_t>(c.T) * H_kv * k * c.B_k * d_h >= (int64_t(1) << 28);
 }
 
 size_t chunk_attend_workspace_bytes(const ChunkSeqs& c, int H_q, int H_kv, int d_h, int k) {

@@ -54,6 +54,10 @@ CASES = [  # new, have, B_k, H_kv, G, d_h, k, pad
     ([200, 100, 1], [64, 2000, 700], 64, 8, 2, 128, 16, 0),
     ([290], [0], 128, 2, 4, 128, 32, 1),
     ([1] * 90 + [60] * 5, [130] * 95, 128, 4, 8, 128, 6, 0),
+    ([520, 60], [500, 300], 128, 4, 8, 128, 8, 2),
+    ([1100], [10], 64, 8, 1, 64, 8, 0),
+    ([1030, 0, 9], [1000, 5, 64], 64, 4, 16, 64, 16, 3),
+    ([1] * 90 + [130] * 5, [130] * 95, 128, 4, 8, 128, 6, 0),
 ]
 
 
@@ -78,7 +82,8 @@ def test_against_float64(msa, new, have, B_k, H_kv, G, d_h, k, pad, holes):
     assert torch.equal(again[live], o[live])
 
 
-@pytest.mark.parametrize("new,have", [([1, 1], [700, 300]), ([200, 30], [300, 500]), ([700, 30], [300, 500])])
+@pytest.mark.parametrize("new,have", [([1, 1], [700, 300]), ([200, 30], [300, 500]), ([700, 30], [300, 500]),
+                                      ([1500, 30], [300, 500])])
 def test_scales_of_any_size(msa, new, have):
     """Value rows from 1e-20 to 1e15, a peaked softmax, large and tiny queries."""
     c = Cache(new, have, 64, 2 if sum(new) < 700 else 4, 64, 64, seed=21)
@@ -100,7 +105,8 @@ def test_scales_of_any_size(msa, new, have):
     check(c, o, lse, attention(c, q, idx, 0.3))
 
 
-@pytest.mark.parametrize("new,have,k", [([3, 1], [100, 64], 3), ([140, 70], [100, 40], 3), ([440, 70], [900, 40], 17)])
+@pytest.mark.parametrize("new,have,k", [([3, 1], [100, 64], 3), ([140, 70], [100, 40], 3), ([440, 70], [900, 40], 17),
+                                        ([900, 70], [900, 40], 17)])
 def test_later_tokens_never_reach_a_row(msa, new, have, k):
     """NaN and infinite rows of later tokens of the same chunk, and stale pages, leave earlier rows alone."""
     c = Cache(new, have, 64, 2, 128, 64, seed=31)
@@ -122,7 +128,7 @@ def test_later_tokens_never_reach_a_row(msa, new, have, k):
 
 
 @pytest.mark.parametrize("new,have,H_kv,k", [([1, 1], [400, 300], 2, 5), ([150, 80], [400, 300], 2, 5),
-                                             ([250, 80], [400, 300], 8, 13)])
+                                             ([250, 80], [400, 300], 8, 13), ([560, 80], [400, 300], 8, 13)])
 def test_bad_pages_and_entries(msa, new, have, H_kv, k):
     c = Cache(new, have, 64, H_kv, 64, 64, seed=41)
     q = torch.randn(c.T, 8 * H_kv, 64, generator=c.g).bfloat16()
@@ -176,7 +182,8 @@ def test_equals_the_decode_step(msa):
     check(c, got, call(msa, c, d, q, idx)[1], ref)
 
 
-@pytest.mark.parametrize("new,have,k", [([1, 1], [400, 300], 5), ([150, 80], [400, 300], 5), ([650, 80], [400, 1300], 24)])
+@pytest.mark.parametrize("new,have,k", [([1, 1], [400, 300], 5), ([150, 80], [400, 300], 5), ([650, 80], [400, 1300], 24),
+                                        ([1300, 80], [400, 1300], 24)])
 def test_refusals_streams_and_graphs(msa, new, have, k):
     c = Cache(new, have, 64, 2, 64, 64, seed=61)
     q = torch.randn(c.T, 16, 64, generator=c.g).bfloat16()
@@ -219,11 +226,12 @@ def test_refusals_streams_and_graphs(msa, new, have, k):
         assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
-def test_wide_page_tables(msa):
+@pytest.mark.parametrize("k", [8, 12])
+def test_wide_page_tables(msa, k):
     """More (group, block) keys than one CTA scans: the same result as with a narrow table."""
     c = Cache([300, 20, 40], [500, 300, 0], 128, 4, 128, 64, seed=91, wide=4096)
     q = torch.randn(c.T, 32, 128, generator=c.g).bfloat16()
-    idx = selection(c, 8)
+    idx = selection(c, k)
     d = c.gpu(c.appended())
     o, lse = call(msa, c, d, q, idx)
     check(c, o, lse, attention(c, q, idx, 128**-0.5))
