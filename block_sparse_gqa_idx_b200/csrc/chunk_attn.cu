@@ -254,8 +254,9 @@ struct Attend {
       for (int n = 0; n < NH; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float mx = fmax3(tx[n][e] - kSlack, s[n][e], s[n][e + 2]);
-          float my = fmax3(ty[n][e] - kSlack, y[n][e], y[n][e + 2]);
+          const bool nox = tx[n][e] == -INFINITY, noy = ty[n][e] == -INFINITY;
+          float mx = fmax3(nox ? -INFINITY : rx[n][e], s[n][e], s[n][e + 2]);
+          float my = fmax3(noy ? -INFINITY : ry[n][e], y[n][e], y[n][e + 2]);
 #pragma unroll
           for (int w = 4; w < 32; w <<= 1) {
             mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, w));
@@ -265,9 +266,9 @@ struct Attend {
           ty[n][e] = my + kSlack;
           mx = mx == -INFINITY ? 0.f : mx;
           my = my == -INFINITY ? 0.f : my;
-          // (nothing is in the sums before the first key, whatever the factor)
-          l[n][e] *= exp2f(fminf(rx[n][e] - mx, 0.f));
-          const float f = exp2f(fminf(ry[n][e] - my, 0.f));
+          // (before the first key there is nothing in the sums to scale)
+          l[n][e] *= nox ? 1.f : exp2f(rx[n][e] - mx);
+          const float f = noy ? 1.f : exp2f(ry[n][e] - my);
 #pragma unroll
           for (int i = 0; i < MT; ++i) {
             o[n][i][e] *= f;

@@ -326,8 +326,8 @@ NRParams params_of(const NormRopeLaunch& a) {
   p.eps = a.eps;
   for (int j = 0; j < p.half; ++j) {
     // inv_freq / (2 pi) modulo one turn, to 2^-64: 64 bits of mantissa
-    long double turns = static_cast<long double>(a.inv_freq[j]) / 6.283185307179586476925286766559L;
-    turns -= floorl(turns);
+    long double turns = static_cast<long double>(a.inv_freq[j]) * 0.15915494309189533576888L;
+    if (!(turns >= 0.0L && turns < 1.0L)) turns -= floorl(turns);
     const long double fixed = turns * 18446744073709551616.0L;
     p.turn[j] = fixed >= 18446744073709551615.0L ? 0 : static_cast<uint64_t>(fixed + 0.5L);
   }

@@ -475,7 +475,9 @@ MSA_API msa_status msa_block_topk(const msa_chunk_dims* dims, const float* score
  *   o    [T, H_q, d_h] bf16, written (rounded once from fp32)
  *   lse  [T, H_q] fp32 natural-log LSE of the scaled logits, or NULL
  * A row whose selection leaves no key gets o = 0 and lse = -inf.  What lies in
- * the pages behind a row's position never reaches it, whatever its bytes. */
+ * the pages behind a row's position never reaches it, whatever its bytes.
+ * Queries must be finite.  A NaN code or scale in a value that a row does see
+ * may make the row's whole output NaN, not only that dimension. */
 MSA_API size_t msa_paged_sparse_attn_fp8_workspace(const msa_chunk_dims* dims);
 MSA_API msa_status msa_paged_sparse_attn_fp8(const msa_chunk_dims* dims, const void* q,
                                              const int32_t* idx, const void* k_pages,

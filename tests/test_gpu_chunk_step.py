@@ -138,3 +138,32 @@ def test_captured_step_serves_growing_sequences(msa):
         torch.cuda.synchronize()
         assert torch.equal(o, ref[0]) and torch.equal(lse, ref[1]) and torch.equal(idx, ref[2])
         assert a["len"].cpu().tolist() == [63 + step, 7 + 2 * step, 9]
+
+
+@pytest.mark.parametrize("T,H_kv,k", [(0, 2, 3), (5, 2, 3), (700, 8, 16)])
+def test_nothing_but_padding(msa, T, H_kv, k):
+    """No rows at all, or only rows that no sequence holds (few, and as many as the forms for long
+    chunks take): nothing is read, and what the caller handed in stays as it was."""
+    c = Cache([0, 0], [300, 5], 128, H_kv, 128, 64, seed=87, pad=T)
+    d = c.gpu()
+    before = [p.clone() for p in c.pools(d)]
+    q, qi = torch.randn(T, 8 * H_kv, 128).bfloat16().cuda(), torch.randn(T, H_kv, 64).bfloat16().cuda()
+    o = torch.full_like(q, 3.0)
+    lse = torch.full((T, 8 * H_kv), 4.0, device="cuda")
+    scores = torch.full((T, H_kv, c.max_pages), 5.0, device="cuda")
+    idx = torch.full((T, H_kv, k), 6, dtype=torch.int32, device="cuda")
+    where = (d["table"], d["cu"], d["len"])
+    assert bool((msa.chunk_positions(d["cu"], d["len"], T) == -1).all())
+    msa.paged_append_fp8(d["new_k"], d["new_v"], d["new_i"], *c.pools(d), *where)
+    rows = msa.paged_gather_fp8(*c.pools(d), *where, T, out=tuple(t.fill_(2.0) for t in (
+        torch.empty_like(d["new_k"]), torch.empty_like(d["new_v"]), torch.empty_like(d["new_i"]))))
+    msa.paged_index_scores_fp8(qi, *c.pools(d)[4:], *where, scores=scores)
+    msa.block_topk(scores, torch.full((T,), -1, dtype=torch.int32, device="cuda"), 128, k, idx_out=idx)
+    msa.paged_sparse_attn_fp8(q, idx, *c.pools(d)[:4], *where, o=o, lse=lse)
+    msa.paged_chunk_fp8(q, qi, d["new_k"], d["new_v"], d["new_i"], *c.pools(d), *where, k, o=o, lse=lse, idx_out=idx)
+    torch.cuda.synchronize()
+    for got, mark in ((o, 3.0), (lse, 4.0), (scores, 5.0), (idx, 6), *((r, 2.0) for r in rows)):
+        assert bool((got == mark).all())
+    for a, b in zip(c.pools(d), before):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    assert d["len"].cpu().tolist() == [300, 5]
