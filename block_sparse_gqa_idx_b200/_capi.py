@@ -707,9 +707,14 @@ def _device_of(t, name: str, ndim: int) -> torch.device:
 def _check(device: torch.device, *specs) -> None:
     """Each spec (tensor, name, dtype, shape): a contiguous tensor of that type
     and shape on `device`."""
+    index = device.index
     for t, name, dtype, shape in specs:
-        if not (isinstance(t, _Tensor) and t.dtype is dtype and t.shape == shape
-                and t.device == device and t.is_contiguous()):
+        try:
+            good = (t.dtype is dtype and t.shape == shape and t.get_device() == index
+                    and t.is_contiguous())
+        except AttributeError:
+            good = False
+        if not good:
             _want(t, name, dtype, shape)
             raise ValueError(f"{name} is on {t.device}, expected {device}")
 
@@ -889,7 +894,7 @@ def chunk_positions(cu_new: torch.Tensor, seq_len: torch.Tensor, T: int, max_len
         raise ValueError("max_len must be a positive multiple of 64")
     with _on(device, stream):
         if pos is None:
-            pos = torch.empty((T,), dtype=_I32, device=device)
+            pos = seq_len.new_empty((T,))
         else:
             _check(device, (pos, "pos", _I32, (T,)))
         _raise("msa_chunk_positions",
@@ -940,9 +945,9 @@ def paged_gather_fp8(k_pages, k_scale, v_pages, v_scale, kidx_pages, kidx_scale,
     S, max_pages = _want_seqs(cu_rows, start, page_table, device)
     with _on(device, stream):
         if out is None:
-            k = torch.empty((T, H_kv, d_h), dtype=_BF16, device=device)
-            v = torch.empty((T, H_kv, d_h), dtype=_BF16, device=device)
-            k_idx = torch.empty((T, d_idx), dtype=_BF16, device=device)
+            k = k_pages.new_empty((T, H_kv, d_h), dtype=_BF16)
+            v = k_pages.new_empty((T, H_kv, d_h), dtype=_BF16)
+            k_idx = k_pages.new_empty((T, d_idx), dtype=_BF16)
         else:
             k, v, k_idx = out
             _check(device, (k, "k", _BF16, (T, H_kv, d_h)), (v, "v", _BF16, (T, H_kv, d_h)),
@@ -973,7 +978,7 @@ def paged_index_scores_fp8(q_idx: torch.Tensor, kidx_pages, kidx_scale, page_tab
     _check(device, (q_idx, "q_idx", _BF16, (T, H_kv, d_idx)))
     with _on(device, stream):
         if scores is None:
-            scores = torch.empty((T, H_kv, max_pages), dtype=_F32, device=device)
+            scores = q_idx.new_empty((T, H_kv, max_pages), dtype=_F32)
         else:
             _check(device, (scores, "scores", _F32, (T, H_kv, max_pages)))
         ws, n = _status_ws(workspace, device)
@@ -998,7 +1003,7 @@ def block_topk(scores: torch.Tensor, pos: torch.Tensor, B_k: int, k: int,
     _check(device, (scores, "scores", _F32, (T, H_kv, n)), (pos, "pos", _I32, (T,)))
     with _on(device, stream):
         if idx_out is None:
-            idx_out = torch.empty((T, H_kv, k), dtype=_I32, device=device)
+            idx_out = pos.new_empty((T, H_kv, k))
         else:
             _check(device, (idx_out, "idx_out", _I32, (T, H_kv, k)))
         _raise("msa_block_topk",
@@ -1045,13 +1050,13 @@ def paged_sparse_attn_fp8(q: torch.Tensor, idx: torch.Tensor, k_pages, k_scale, 
     sizes = (S, T, max_pages, P, H_q, H_kv, d_h, 64, B_k, kk, attn_scale)
     with _on(device, stream):
         if o is None:
-            o = torch.empty((T, H_q, d_h), dtype=_BF16, device=device)
+            o = torch.empty_like(q)
         else:
             _check(device, (o, "o", _BF16, (T, H_q, d_h)))
         if lse is not None:
             _check(device, (lse, "lse", _F32, (T, H_q)))
         elif want_lse:
-            lse = torch.empty((T, H_q), dtype=_F32, device=device)
+            lse = q.new_empty((T, H_q), dtype=_F32)
         ws = _scratch(_attn_bytes(device.index, *sizes), device, workspace)
         _raise("msa_paged_sparse_attn_fp8",
                LIB.msa_paged_sparse_attn_fp8(_chunk_ref(*sizes), q.data_ptr(), idx.data_ptr(),
@@ -1087,15 +1092,15 @@ def paged_chunk_fp8(q, q_idx, k_new, v_new, k_idx_new, k_pages, k_scale, v_pages
     sizes = (S, T, max_pages, P, H_q, H_kv, d_h, d_idx, B_k, kk, attn_scale, idx_scale)
     with _on(device, stream):
         if o is None:
-            o = torch.empty((T, H_q, d_h), dtype=_BF16, device=device)
+            o = torch.empty_like(q)
         else:
             _check(device, (o, "o", _BF16, (T, H_q, d_h)))
         if lse is not None:
             _check(device, (lse, "lse", _F32, (T, H_q)))
         elif want_lse:
-            lse = torch.empty((T, H_q), dtype=_F32, device=device)
+            lse = q.new_empty((T, H_q), dtype=_F32)
         if idx_out is None:
-            idx_out = torch.empty((T, H_kv, kk), dtype=_I32, device=device)
+            idx_out = cu_new.new_empty((T, H_kv, kk))
         else:
             _check(device, (idx_out, "idx_out", _I32, (T, H_kv, kk)))
         ws = _scratch(_chunk_bytes(device.index, *sizes), device, workspace)
