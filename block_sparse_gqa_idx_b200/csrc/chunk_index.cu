@@ -474,7 +474,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           const int st = g % ST;
           ok = mbar_wait(&k_empty[st], ((g / ST) & 1) ^ 1, abort_flag, p.status, 200);
           ok = __all_sync(0xFFFFFFFFu, ok);
-          if (ok && lane == 0) {
+          if (!ok) break;
+          if (lane == 0) {
             sOk[st] = have;
             mbar_arrive_expect_tx(&k_full[st], __popc(have) * (BK * D + BK * 4));
 #pragma unroll
@@ -487,6 +488,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
         }
     }
+    // nothing is still on its way into this CTA's shared memory when it ends, not
+    // even after a wait that gave up
+    for (uint32_t j = g > ST ? g - ST : 0; j < g; ++j)
+      mbar_wait(&k_full[j % ST], (j / ST) & 1, nullptr, p.status, 203);
   } else if (warp == 1) {
     // ------------------------------------------------------------- MMA --
     if (lane == 0) {
@@ -923,8 +928,9 @@ cudaError_t launch_scores_typed(const ScoreLaunch& a, cudaStream_t s) {
     chunk_scores_tc_kernel<D, BK><<<sms, kTcThreads, SH::SMEM, s>>>(tk, p);
     prof_end(s);
     e = cudaGetLastError();
-    // a single sequence of so many rows leaves the other form nothing
-    if (e != cudaSuccess || a.c.S == 1) return e;
+    // The other form follows for one sequence too: the call's rows may be padding
+    // for the most part.
+    if (e != cudaSuccess) return e;
   }
   // Columns per tile: 8 while there are no more tokens than sequences (single
   // tokens share no keys, and fewer registers let twice as many warps load), else

@@ -60,6 +60,8 @@ CASES = [  # new, have, B_k, H_kv, d_idx, pad
     ([33, 130], [1000, 65], 64, 2, 128, 0),
     ([300, 5, 129], [20, 900, 0], 128, 4, 64, 7),
     ([600], [1300], 128, 4, 128, 0),
+    ([3], [1000], 128, 4, 64, 200),  # one sequence, whose rows are few, and much padding
+    ([100], [700], 64, 2, 128, 300),
     ([257, 400], [64, 2000], 64, 8, 64, 5),
     ([700, 1], [0, 3000], 128, 1, 64, 0),
     ([100, 1, 90], [3000, 700, 0], 64, 3, 64, 4),
