@@ -890,6 +890,7 @@ def chunk_positions(cu_new: torch.Tensor, seq_len: torch.Tensor, T: int, max_len
     device = _device_of(seq_len, "seq_len", 1)
     S = seq_len.shape[0]
     _check(device, (seq_len, "seq_len", _I32, (S,)), (cu_new, "cu_new", _I32, (S + 1,)))
+    T, max_len = int(T), int(max_len)
     if max_len < 64 or max_len % 64 != 0:
         raise ValueError("max_len must be a positive multiple of 64")
     with _on(device, stream):
@@ -943,6 +944,7 @@ def paged_gather_fp8(k_pages, k_scale, v_pages, v_scale, kidx_pages, kidx_scale,
     P, B_k, H_kv, d_h, d_idx = _want_pools(k_pages, k_scale, v_pages, v_scale, kidx_pages,
                                            kidx_scale, device)
     S, max_pages = _want_seqs(cu_rows, start, page_table, device)
+    T = int(T)
     with _on(device, stream):
         if out is None:
             k = k_pages.new_empty((T, H_kv, d_h), dtype=_BF16)
@@ -976,6 +978,7 @@ def paged_index_scores_fp8(q_idx: torch.Tensor, kidx_pages, kidx_scale, page_tab
     P, B_k, d_idx = _want_index_pages(kidx_pages, kidx_scale, device)
     S, max_pages = _want_seqs(cu_new, seq_len, page_table, device)
     _check(device, (q_idx, "q_idx", _BF16, (T, H_kv, d_idx)))
+    idx_scale = float(idx_scale)
     with _on(device, stream):
         if scores is None:
             scores = q_idx.new_empty((T, H_kv, max_pages), dtype=_F32)
@@ -1001,6 +1004,7 @@ def block_topk(scores: torch.Tensor, pos: torch.Tensor, B_k: int, k: int,
     device = _device_of(scores, "scores", 3)
     T, H_kv, n = scores.shape
     _check(device, (scores, "scores", _F32, (T, H_kv, n)), (pos, "pos", _I32, (T,)))
+    B_k, k = int(B_k), int(k)
     with _on(device, stream):
         if idx_out is None:
             idx_out = pos.new_empty((T, H_kv, k))
@@ -1047,7 +1051,7 @@ def paged_sparse_attn_fp8(q: torch.Tensor, idx: torch.Tensor, k_pages, k_scale, 
     P, B_k, H_kv, d_h = _want_pages(k_pages, k_scale, v_pages, v_scale, device)
     S, max_pages = _want_seqs(cu_new, seq_len, page_table, device)
     _check(device, (q, "q", _BF16, (T, H_q, d_h)), (idx, "idx", _I32, (T, H_kv, kk)))
-    sizes = (S, T, max_pages, P, H_q, H_kv, d_h, 64, B_k, kk, attn_scale)
+    sizes = (S, T, max_pages, P, H_q, H_kv, d_h, 64, B_k, kk, float(attn_scale))
     with _on(device, stream):
         if o is None:
             o = torch.empty_like(q)
@@ -1089,7 +1093,8 @@ def paged_chunk_fp8(q, q_idx, k_new, v_new, k_idx_new, k_pages, k_scale, v_pages
     _check(device, (q, "q", _BF16, (T, H_q, d_h)), (q_idx, "q_idx", _BF16, (T, H_kv, d_idx)),
            (k_new, "k_new", _BF16, (T, H_kv, d_h)), (v_new, "v_new", _BF16, (T, H_kv, d_h)),
            (k_idx_new, "k_idx_new", _BF16, (T, d_idx)))
-    sizes = (S, T, max_pages, P, H_q, H_kv, d_h, d_idx, B_k, kk, attn_scale, idx_scale)
+    kk = int(kk)
+    sizes = (S, T, max_pages, P, H_q, H_kv, d_h, d_idx, B_k, kk, float(attn_scale), float(idx_scale))
     with _on(device, stream):
         if o is None:
             o = torch.empty_like(q)

@@ -311,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int4 meta_next = meta_of(0), meta_next2 = meta_of(1);
       uint32_t next_slot = 0;
       if (my_tiles > 0 && lane < meta_next.z) next_slot = p.c.entries[meta_next.y + lane];
-      int kv_key = -1, gen = -1;
+      int kv_key = -1, gen = -1, sent = 0;
       for (int n = 0; n < my_tiles; ++n) {
         const int key = meta_next.x, len = meta_next.z;
         const uint32_t myslot = next_slot;
@@ -356,7 +356,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                           c * 64, h0, i);
           }
         }
+        ++sent;
       }
+      // nothing is still on its way into this CTA's shared memory when it ends,
+      // not even after a wait that gave up (so below for the pages)
+      for (int j = sent > QS ? sent - QS : 0; j < sent; ++j)
+        mbar_wait(&q_full[j % QS], (j / QS) & 1, nullptr, p.status, 156);
     } else if (warp == 6) {
       // ------------------------------------------- raw pages (TMA), ahead --
       if (lane == 0) {
@@ -378,6 +383,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           n = run_end(n, meta);
         }
+        for (int j = ring > kRaw ? ring - kRaw : 0; j < ring; ++j)
+          mbar_wait(&raw_full[j % kRaw], (j / kRaw) & 1, nullptr, p.status, 157);
       }
     } else if (warp == 7) {
       // ------------------------------------------------------ page scales --
