@@ -23,8 +23,8 @@
 // partial stays within 128 * 448 < 65504.
 //
 // 4096 rows of two sequences at 61K cached tokens (H_q = 32, H_kv = 4, d_h =
-// B_k = 128, k = 16; 137 GFLOP): 349 us in the tile kernel, of 497 in all (the
-// query-outer kernel: 1406); the merge reads its 537 MB of partials in 131.
+// B_k = 128, k = 16; 137 GFLOP): 349 us in the tile kernel, of 458 in all (the
+// query-outer kernel: 1406); the merge reads its 537 MB of partials in 88.
 // What bounds the tiles is the MMAs beside the softmax's TMEM reads: S and O
 // take 1200 and 1500 clocks a tile in place, 512 each at the peak rate.
 #include <climits>
@@ -791,53 +791,46 @@ __global__ void __launch_bounds__(256) chunk_tables_kernel(const ChunkSeqs c, in
 
 // The inverse index of few keys (up to kFewKeys; more go through
 // inv_index.cu's multi-CTA scan), in three short kernels:
-//   rank   every selection's place in its key's list, by counting: a warp
-//          takes one (group, slot) of 32 consecutive rows, which mostly agree
-//          on the hot blocks (the first one, their own), so that those cost
-//          one atomic a warp;
+//   rank   every selection's key and its place in the key's list, by counting:
+//          a warp takes one (group, slot) of 32 consecutive rows, which mostly
+//          agree on the hot blocks (the first one, their own), so that those
+//          cost one atomic a warp;
 //   scan   one CTA: where each key's list and its tiles start;
 //   place  the selections to their places, and the tiles' records.
 constexpr int64_t kFewKeys = 32768;
-constexpr int kPlaceRows = 32;  // rows per CTA of rank and place
+constexpr int kPlaceRows = 32;  // rows per CTA of rank
 
-// Calls f(key, selection, its index in `rank`) for the CTA's selections, warp by
-// warp with all lanes (key -1: none), from a shared-memory copy of its rows.
-template <typename F>
-__device__ __forceinline__ void for_selections(const InvParams& p, bool report_bad, F f) {
+// `rank`: {key or -1, place}, a CTA's selections as [group, slot][row].
+__global__ void __launch_bounds__(1024) chunk_rank_kernel(const InvParams p, int2* rank) {
   extern __shared__ int32_t sel[];  // [kPlaceRows][H_kv * k]
+  griddep_wait();
   const int per_q = p.H_kv * p.kk;
   const int64_t row0 = static_cast<int64_t>(blockIdx.x) * kPlaceRows;
   const int rows = static_cast<int>(p.nq - row0 < kPlaceRows ? p.nq - row0 : kPlaceRows);
   const int32_t* src = p.idx + (p.q0 + row0) * per_q;
   for (int i = threadIdx.x; i < rows * per_q; i += blockDim.x) sel[i] = __ldg(src + i);
-  __syncthreads();
   const int lane = threadIdx.x & 31;
   const int t = static_cast<int>(p.q0 + row0) + lane;
   const int2 sq = lane < rows ? __ldg(p.qinfo + t) : make_int2(INT_MAX, 0);
   const int own = lane < rows && t >= sq.x ? (t - sq.x) / p.B_k : -1;
+  __syncthreads();
   for (int c = threadIdx.x >> 5; c < per_q; c += blockDim.x >> 5) {
     const int b = lane < rows ? sel[lane * per_q + c] : -1;
     int key = -1;
     if (b < -1 || b >= p.B_seq) {
-      if (report_bad) report(p.status, DEV_ERR_BAD_INDEX, 141, t, b);
+      report(p.status, DEV_ERR_BAD_INDEX, 141, t, b);
     } else if (b >= 0 && b <= own) {
       if (__ldg(&p.blk[sq.y + b].x) >= 0) key = c / p.kk * static_cast<int>(p.B) + sq.y + b;
-      else if (report_bad) report(p.status, DEV_ERR_BAD_INDEX, 142, t, b);
+      else report(p.status, DEV_ERR_BAD_INDEX, 142, t, b);
     }
-    f(key, (row0 + lane) * per_q + c, (static_cast<int64_t>(blockIdx.x) * per_q + c) * 32 + lane);
-  }
-}
-
-__global__ void __launch_bounds__(1024) chunk_rank_kernel(const InvParams p, uint32_t* rank) {
-  griddep_wait();
-  for_selections(p, true, [&](int key, int64_t, int64_t at) {
     const unsigned peers = __match_any_sync(0xFFFFFFFFu, key);
-    const int lane = threadIdx.x & 31, leader = __ffs(peers) - 1;
+    const int leader = __ffs(peers) - 1;
     int base = 0;
     if (lane == leader && key >= 0) base = atomicAdd(&p.c.counts[key], __popc(peers));
     base = __shfl_sync(0xFFFFFFFFu, base, leader);
-    if (key >= 0) rank[at] = base + __popc(peers & ((1u << lane) - 1));
-  });
+    rank[(static_cast<int64_t>(blockIdx.x) * per_q + c) * 32 + lane] =
+        make_int2(key, base + __popc(peers & ((1u << lane) - 1)));
+  }
 }
 
 __global__ void __launch_bounds__(1024) chunk_scan_kernel(const InvParams p, int nkeys) {
@@ -904,19 +897,47 @@ __global__ void __launch_bounds__(1024) chunk_scan_kernel(const InvParams p, int
   }
 }
 
-__global__ void __launch_bounds__(1024) chunk_place_kernel(const InvParams p, const uint32_t* rank,
-                                                          int nkeys) {
+// A thread per selection and, for the records, a thread per key; the tiles of a
+// long list are written by the key's warp.
+__global__ void __launch_bounds__(256) chunk_place_kernel(const InvParams p, const int2* rank,
+                                                         int64_t n_rank, int nkeys) {
   griddep_wait();
-  for_selections(p, false, [&](int key, int64_t e, int64_t at) {
-    if (key >= 0) p.c.entries[p.c.offsets[key] + rank[at]] = static_cast<uint32_t>(e);
-  });
-  const int n_tiles = p.c.n_tiles[0];
-  for (int t = blockIdx.x * blockDim.x + threadIdx.x; t < n_tiles; t += gridDim.x * blockDim.x) {
-    const int key = find_key(p.c.tile_off, nkeys, t);
-    const int t0 = p.c.tile_off[key], t1 = p.c.tile_off[key + 1];
-    const int first = p.c.offsets[key] + (t - t0) * p.Tq;
-    const int left = p.c.offsets[key + 1] - first;
-    p.c.tile_meta[t] = make_int4(key, first, left < p.Tq ? left : p.Tq, t1);
+  constexpr int kOwn = 4;  // records that a key's thread writes itself
+  const int per_q = p.H_kv * p.kk;
+  const int lane = threadIdx.x & 31;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+  if (i < n_rank) {
+    const int2 k = __ldg(rank + i);
+    if (k.x >= 0) {
+      const int64_t col = i >> 5, block = col / per_q;
+      const int64_t e = (block * kPlaceRows + (i & 31)) * per_q + (col - block * per_q);
+      p.c.entries[p.c.offsets[k.x] + k.y] = static_cast<uint32_t>(e);
+    }
+  }
+  const int64_t threads = static_cast<int64_t>(gridDim.x) * blockDim.x;
+  for (int64_t k0 = i - lane; k0 < nkeys; k0 += threads) {  // whole warps
+    const int key = static_cast<int>(k0) + lane;
+    int t0 = 0, t1 = 0, first = 0, end = 0;
+    if (key < nkeys) {
+      t0 = p.c.tile_off[key];
+      t1 = p.c.tile_off[key + 1];
+      first = p.c.offsets[key];
+      end = p.c.offsets[key + 1];
+    }
+    auto put = [&](int key_, int t, int at, int end_, int t1_) {
+      p.c.tile_meta[t] = make_int4(key_, at, end_ - at < p.Tq ? end_ - at : p.Tq, t1_);
+    };
+#pragma unroll
+    for (int j = 0; j < kOwn; ++j)
+      if (t0 + j < t1) put(key, t0 + j, first + j * p.Tq, end, t1);
+    unsigned more = __ballot_sync(0xFFFFFFFFu, t1 - t0 > kOwn);
+    for (; more != 0; more &= more - 1) {
+      const int src = __ffs(more) - 1;
+      const int a = __shfl_sync(0xFFFFFFFFu, t0, src), b = __shfl_sync(0xFFFFFFFFu, t1, src);
+      const int f = __shfl_sync(0xFFFFFFFFu, first, src), z = __shfl_sync(0xFFFFFFFFu, end, src);
+      for (int j = kOwn + lane; a + j < b; j += 32)
+        put(static_cast<int>(k0) + src, a + j, f + j * p.Tq, z, b);
+    }
   }
 }
 
@@ -924,7 +945,7 @@ struct MergeParams {
   __nv_bfloat16* o;
   float* lse;
   int q0, nq;
-  int H_q, H_kv, kk, G;
+  int H_q, H_kv, kk;
   const int2* qinfo;
   const __half* part_o;
   const float* part_lse;
@@ -933,97 +954,107 @@ struct MergeParams {
 
 // Merge: one thread per 8 consecutive outputs of a head, the G * D / 8 threads
 // of a (row, group) in the partials' order [d/8][g].  The first slots' partials
-// (16 bytes each, coalesced) are on their way while the CTA turns the slots'
-// LSEs into weights in shared memory, once per (slot, head).
-template <int D>
+// (16 bytes each, coalesced) are on their way while the slots' LSEs become
+// weights: the R lanes of a warp that share a head take R slots at a time, their
+// maximum and sum are shuffles, and a slot's weight comes from its lane when its
+// partial is due.  No barrier: with the weights in shared memory, made once per
+// CTA, the 537 MB of the case above took 129 us, this 88 (6.1 TB/s).
+template <int D, int G>
 __global__ void __launch_bounds__(256) chunk_merge_kernel(const MergeParams p) {
   griddep_wait();
   constexpr int NB = 8;  // slots in flight
-  __shared__ float wt[32][32];     // [slot][unit * G + g]: weight times factor
-  __shared__ float zs[32][32];     // the slots' LSEs
-  __shared__ float top[32], sum[32];
-  const int per_unit = p.G * D / 8;
-  const int units = blockDim.x / per_unit;  // (row, group) units of this CTA
-  const int u = threadIdx.x / per_unit, e = threadIdx.x - u * per_unit;
-  const int64_t unit0 = static_cast<int64_t>(blockIdx.x) * units;
-  const int64_t n_units = static_cast<int64_t>(p.nq) * p.H_kv;
-  const int64_t unit = unit0 + u;
-  const bool on = unit < n_units;
-  const int64_t stride = static_cast<int64_t>(p.G) * D;
-  const __half* base = p.part_o + (on ? unit : 0) * p.kk * stride + e * 8;
+  constexpr int PER_UNIT = G * D / 8;
+  constexpr int LANES = PER_UNIT < 32 ? PER_UNIT : 32;  // of a unit in one warp
+  constexpr int R = LANES / G;
+  constexpr int NJ = (32 + R - 1) / R;  // slots per lane
+  const int lane = threadIdx.x & 31, el = lane % LANES;
+  const int u = threadIdx.x / PER_UNIT, e = threadIdx.x - u * PER_UNIT;
+  const int64_t unit = static_cast<int64_t>(blockIdx.x) * (blockDim.x / PER_UNIT) + u;
+  const bool on = unit < static_cast<int64_t>(p.nq) * p.H_kv;
+  constexpr int64_t stride = static_cast<int64_t>(G) * D;
+  const int64_t slot0 = (on ? unit : 0) * p.kk;
+  const __half* base = p.part_o + slot0 * stride + e * 8;
   uint4 x[NB];
 #pragma unroll
   for (int j = 0; j < NB; ++j)
     x[j] = j < p.kk ? __ldcs(reinterpret_cast<const uint4*>(base + j * stride))
                     : make_uint4(0, 0, 0, 0);
-  const int cols = units * p.G;
-  for (int i = threadIdx.x; i < cols * p.kk; i += blockDim.x) {
-    const int s = i / cols, c = i - s * cols;
-    const int64_t un = unit0 + c / p.G;
-    float z = -INFINITY, f = 0.f;
-    if (un < n_units) {
-      const int64_t at = (un * p.kk + s) * p.G + c % p.G;
-      z = p.part_lse[at];  // -inf: an unused slot, the rest of it was never written
-      f = p.part_f[at];
+  const int g = e % G;
+  float z[NJ], w[NJ];
+  float m = -INFINITY, l = 0.f;
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) {
+    const int s = j * R + el / G;
+    z[j] = -INFINITY;  // -inf: an unused slot, the rest of it was never written
+    w[j] = 0.f;
+    if (s < p.kk) {
+      const int64_t at = (slot0 + s) * G + g;
+      z[j] = p.part_lse[at];
+      w[j] = p.part_f[at];
     }
-    zs[s][c] = z;
-    wt[s][c] = z == -INFINITY ? 0.f : f;
+    m = fmaxf(m, z[j]);
   }
-  __syncthreads();
-  if (threadIdx.x < cols) {
-    const int c = threadIdx.x;
-    float m = -INFINITY, l = 0.f;
-    for (int s = 0; s < p.kk; ++s) m = fmaxf(m, zs[s][c]);
-    const float ms = m == -INFINITY ? 0.f : m;
-    for (int s = 0; s < p.kk; ++s) {
-      const float w = exp2f(zs[s][c] - ms);
-      l += w;
-      wt[s][c] = wt[s][c] == 0.f ? 0.f : w * wt[s][c];
-    }
-    top[c] = m;
-    sum[c] = l;
+#pragma unroll
+  for (int o = G; o < LANES; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+  const float ms = m == -INFINITY ? 0.f : m;
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) {
+    const float t = exp2f(z[j] - ms);
+    l += t;
+    w[j] = z[j] == -INFINITY ? 0.f : t * w[j];
   }
-  __syncthreads();
-  if (!on) return;
-  const int g = e % p.G, d0 = e / p.G * 8, c = u * p.G + g;
+#pragma unroll
+  for (int o = G; o < LANES; o <<= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
   float acc[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) acc[j] = 0.f;
-  for (int s0 = 0; s0 < p.kk; s0 += NB) {
+#pragma unroll
+  for (int s0 = 0; s0 < 32; s0 += NB) {
+    if (s0 >= p.kk) break;
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
       const int s = s0 + j;
-      if (s < p.kk) {
-        const float w = wt[s][c];
-        const __half2* h = reinterpret_cast<const __half2*>(&x[j]);
-        if (w != 0.f)  // nothing of an unused slot
+      const float ws = __shfl_sync(0xFFFFFFFFu, w[s / R], lane - el + s % R * G + g);
+      const __half2* h = reinterpret_cast<const __half2*>(&x[j]);
+      if (ws != 0.f)  // nothing of an unused slot
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const float2 v = __half22float2(h[q]);
-            acc[2 * q] = fmaf(w, v.x, acc[2 * q]);
-            acc[2 * q + 1] = fmaf(w, v.y, acc[2 * q + 1]);
-          }
-        if (s + NB < p.kk)
-          x[j] = __ldcs(reinterpret_cast<const uint4*>(base + (s + NB) * stride));
-      }
+        for (int q = 0; q < 4; ++q) {
+          const float2 v = __half22float2(h[q]);
+          acc[2 * q] = fmaf(ws, v.x, acc[2 * q]);
+          acc[2 * q + 1] = fmaf(ws, v.y, acc[2 * q + 1]);
+        }
+      if (s + NB < p.kk)
+        x[j] = __ldcs(reinterpret_cast<const uint4*>(base + (s + NB) * stride));
     }
   }
+  if (!on) return;
   const int il = static_cast<int>(unit / p.H_kv);
   const int r = static_cast<int>(unit - static_cast<int64_t>(il) * p.H_kv);
   const int t = p.q0 + il;
   if (t < __ldg(&p.qinfo[t].x)) return;  // a skipped row
-  const float l = sum[c];
+  const int d0 = e / G * 8;
   const float inv = l == 0.f ? 0.f : 1.f / l;
-  const int64_t head = static_cast<int64_t>(t) * p.H_q + r * p.G + g;
+  const int64_t head = static_cast<int64_t>(t) * p.H_q + r * G + g;
   *reinterpret_cast<uint4*>(p.o + head * D + d0) =
       make_uint4(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv),
                  pack_bf16(acc[4] * inv, acc[5] * inv), pack_bf16(acc[6] * inv, acc[7] * inv));
-  if (p.lse != nullptr && d0 == 0) p.lse[head] = l == 0.f ? -INFINITY : (top[c] + log2f(l)) * kLn2;
+  if (p.lse != nullptr && d0 == 0) p.lse[head] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
+template <int D>
+auto merge_kernel(int G) {
+  switch (G) {
+    case 1: return chunk_merge_kernel<D, 1>;
+    case 2: return chunk_merge_kernel<D, 2>;
+    case 4: return chunk_merge_kernel<D, 4>;
+    case 8: return chunk_merge_kernel<D, 8>;
+    default: return chunk_merge_kernel<D, 16>;  // the form takes divisors of 16
+  }
 }
 
 struct KVBufs {
   ChunkBufs c;
-  uint32_t* rank;
+  int2* rank;
   float* part_f;
   int2* qinfo;
   int4* blk;
@@ -1040,7 +1071,7 @@ KVBufs carve_kv(void* ws, int T, int64_t B, int H_q, int H_kv, int d_h, int kk, 
     off += align256(bytes);
     return r;
   };
-  b.rank = reinterpret_cast<uint32_t*>(take(sizeof(uint32_t) * (Nc + kPlaceRows) * H_kv * kk));
+  b.rank = reinterpret_cast<int2*>(take(sizeof(int2) * (Nc + kPlaceRows) * H_kv * kk));
   b.part_f = reinterpret_cast<float*>(take(sizeof(float) * Nc * kk * H_q));
   b.qinfo = reinterpret_cast<int2*>(take(sizeof(int2) * T));
   b.blk = reinterpret_cast<int4*>(take(sizeof(int4) * B));
@@ -1144,8 +1175,9 @@ cudaError_t launch_typed(const AttendLaunch& a, cudaStream_t stream) {
       prof_end(stream);
       if (e != cudaSuccess) return e;
       prof_begin("chunk_place", stream);
-      e = launch_pdl(chunk_place_kernel, dim3(blocks), dim3(1024), rows, stream, ip,
-                     static_cast<const uint32_t*>(b.rank), static_cast<int>(nkeys));
+      const int64_t n_rank = static_cast<int64_t>(blocks) * kPlaceRows * a.H_kv * a.k;
+      e = launch_pdl(chunk_place_kernel, dim3(static_cast<unsigned>((n_rank + 255) / 256)), dim3(256), 0,
+                     stream, ip, static_cast<const int2*>(b.rank), n_rank, static_cast<int>(nkeys));
       prof_end(stream);
       if (e != cudaSuccess) return e;
     } else {
@@ -1185,7 +1217,6 @@ cudaError_t launch_typed(const AttendLaunch& a, cudaStream_t stream) {
     mp.H_q = a.H_q;
     mp.H_kv = a.H_kv;
     mp.kk = a.k;
-    mp.G = G;
     mp.qinfo = b.qinfo;
     mp.part_o = b.c.part_o;
     mp.part_lse = b.c.part_lse;
@@ -1194,7 +1225,7 @@ cudaError_t launch_typed(const AttendLaunch& a, cudaStream_t stream) {
     const int block = per_unit > 128 ? per_unit : 128;
     const int64_t units = block / per_unit;
     prof_begin("chunk_merge", stream);
-    e = launch_pdl(chunk_merge_kernel<D_H>,
+    e = launch_pdl(merge_kernel<D_H>(G),
                    dim3(static_cast<unsigned>((nq * a.H_kv + units - 1) / units)), dim3(block), 0,
                    stream, mp);
     prof_end(stream);

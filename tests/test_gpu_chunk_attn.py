@@ -58,6 +58,10 @@ CASES = [  # new, have, B_k, H_kv, G, d_h, k, pad
     ([1100], [10], 64, 8, 1, 64, 8, 0),
     ([1030, 0, 9], [1000, 5, 64], 64, 4, 16, 64, 16, 3),
     ([1] * 90 + [130] * 5, [130] * 95, 128, 4, 8, 128, 6, 0),
+    # every number of heads per group with either head size
+    ([1030], [10], 64, 8, 1, 128, 8, 2),
+    ([1100, 3], [10, 700], 64, 8, 2, 64, 8, 0),
+    ([600], [500], 128, 4, 4, 64, 16, 1),
 ]
 
 
