@@ -45,5 +45,6 @@ def __getattr__(name):
     if name in _CAPI:
         from . import _capi
 
-        return getattr(_capi, name)
+        value = globals()[name] = getattr(_capi, name)  # found directly from now on
+        return value
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

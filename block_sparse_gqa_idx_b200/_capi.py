@@ -679,6 +679,7 @@ def quantize_fp8_rows(x: torch.Tensor, codes: Optional[torch.Tensor] = None,
 _NO_CONTEXT = contextlib.nullcontext()
 _BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
 _Tensor = torch.Tensor
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                       lambda index: torch.cuda.current_stream(index).cuda_stream)
 
@@ -690,7 +691,7 @@ def _on(device: torch.device, stream):
         if stream.device != device:
             raise ValueError(f"stream is on {stream.device}, the tensors are on {device}")
         return torch.cuda.stream(stream)
-    if device.index == torch.cuda.current_device():
+    if device.index == _current_device():
         return _NO_CONTEXT
     return torch.cuda.device(device)
 
@@ -710,13 +711,13 @@ def _check(device: torch.device, *specs) -> None:
     index = device.index
     for t, name, dtype, shape in specs:
         try:
-            good = (t.dtype is dtype and t.shape == shape and t.get_device() == index
-                    and t.is_contiguous())
+            if (t.dtype is dtype and t.shape == shape and t.get_device() == index
+                    and t.is_contiguous()):
+                continue
         except AttributeError:
-            good = False
-        if not good:
-            _want(t, name, dtype, shape)
-            raise ValueError(f"{name} is on {t.device}, expected {device}")
+            pass
+        _want(t, name, dtype, shape)
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
 
 
 def _scratch(nbytes: int, device: torch.device, ws: Optional[torch.Tensor]) -> torch.Tensor:
