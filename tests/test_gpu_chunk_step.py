@@ -167,3 +167,25 @@ def test_nothing_but_padding(msa, T, H_kv, k):
     for a, b in zip(c.pools(d), before):
         assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
     assert d["len"].cpu().tolist() == [300, 5]
+
+
+@pytest.mark.parametrize("new,have", [([1, 2], [300, 127]), ([560, 40], [300, 900])])
+def test_pages_beyond_four_gigabytes(msa, new, have):
+    """Pages whose byte offsets pass 32 bits give what the same pages give in a small pool."""
+    c = Cache(new, have, 128, 8, 128, 64, seed=41)
+    q, qi = torch.randn(c.T, 16, 128, generator=c.g).bfloat16().cuda(), torch.randn(c.T, 8, 64, generator=c.g).bfloat16().cuda()
+    small = c.gpu()
+    at = (1 << 32) // (128 * 8 * 128) + 3  # the first page of the sequences in the large pool
+    big = dict(small, len=small["len"].clone(), table=small["table"] + at)
+    for n in ("kp", "ks", "vp", "vs", "ip", "is"):
+        big[n] = torch.empty(at + c.n_pages, *small[n].shape[1:], dtype=small[n].dtype, device="cuda")
+        big[n][at:] = small[n]
+    assert big["kp"][at:].data_ptr() - big["kp"].data_ptr() > 1 << 32
+    got = []
+    for d in (small, big):
+        got.append(msa.paged_chunk_fp8(q, qi, d["new_k"], d["new_v"], d["new_i"], *c.pools(d), d["table"], d["cu"],
+                                       d["len"], 6))
+        cu = torch.tensor([0, 200, 320], dtype=torch.int32).cuda()
+        got[-1] += msa.paged_gather_fp8(*c.pools(d), d["table"], cu, torch.zeros(2, dtype=torch.int32).cuda(), 320)
+    for a, b in zip(*got):
+        assert bool(torch.isfinite(a).all()) and torch.equal(a, b)
