@@ -582,10 +582,10 @@ cudaError_t launch_direct(const AttendLaunch& a, cudaStream_t s) {
 // every row reads them (through L2); the KV-outer form costs about 30 us of short
 // kernels and each page once, and pays from about 2^28 such values on (H_q = 32,
 // H_kv = 4, d_h = B_k = 128, k = 16: 256 rows).  Measured there, query-outer against
-// KV-outer, one sequence at 9K / four at 9K / one at 61K: 128 rows 53 : 47 / 53 : 62 /
-// 54 : 90 us, 256 rows 92 : 57 / 93 : 82 / 94 : 92, 512 rows 150 : 82 / 152 : 112 /
-// 152 : 137; H_q = 8, H_kv = 2, 256 rows 51 : 40 / 52 : 50 / 51 : 55; d_h = B_k = 64,
-// k = 8, 512 rows 39 : 44 / 39 : 59 / 39 : 91.
+// KV-outer, one sequence at 9K / four at 9K / one at 61K: 128 rows 53 : 46 / 54 : 56 /
+// 54 : 83 us, 256 rows 93 : 51 / 95 : 74 / 95 : 87, 512 rows 151 : 76 / 153 : 107 /
+// 152 : 127; H_q = 8, H_kv = 2, 256 rows 52 : 37 / 52 : 45 / 52 : 51; d_h = B_k = 64,
+// k = 8, 512 rows 40 : 44 / 40 : 60 / 41 : 93.
 static bool kv_outer(const msa::ChunkSeqs& c, int H_q, int H_kv, int d_h, int k) {
   const int G = H_q / H_kv;
   if (16 % G != 0 || (G < 8 && H_q % 8 != 0)) return false;  // its MMA rows and TMA boxes
