@@ -815,7 +815,8 @@ __global__ void __launch_bounds__(1024) chunk_rank_kernel(const InvParams p, int
   const int own = lane < rows && t >= sq.x ? (t - sq.x) / p.B_k : -1;
   __syncthreads();
   for (int c = threadIdx.x >> 5; c < per_q; c += blockDim.x >> 5) {
-    const int b = lane < rows ? sel[lane * per_q + c] : -1;
+    // a skipped row's entries were never written: they are not looked at
+    const int b = own >= 0 ? sel[lane * per_q + c] : -1;
     int key = -1;
     if (b < -1 || b >= p.B_seq) {
       report(p.status, DEV_ERR_BAD_INDEX, 141, t, b);

@@ -14,14 +14,16 @@ namespace msa {
 namespace {
 
 // The key (r * B + global block) of query i's selection b in group r, or -1
-// when it selects nothing.
+// when it selects nothing.  A row whose sequence begins after it is skipped by
+// its call (padding): its entries were never written and are not looked at.
 __device__ __forceinline__ int inv_block(const InvParams& p, int64_t i, int r, int32_t b,
                                          bool report_bad) {
+  const int2 sq = seq_of(p.qinfo, i);
+  if (i < sq.x) return -1;
   if (b < -1 || b >= (p.B_seq > 0 ? p.B_seq : p.B)) {
     if (report_bad) report(p.status, DEV_ERR_BAD_INDEX, 40, static_cast<int>(i), b);
     return -1;
   }
-  const int2 sq = seq_of(p.qinfo, i);
   if (b < 0 || b > (i - sq.x) / p.B_k) return -1;
   if (p.blk != nullptr && p.blk[sq.y + b].x < 0) {
     if (report_bad) report(p.status, DEV_ERR_BAD_INDEX, 41, static_cast<int>(i), b);

@@ -471,7 +471,8 @@ MSA_API msa_status msa_block_topk(const msa_chunk_dims* dims, const float* score
  *   idx  [T, H_kv, k] int32: blocks of the row's sequence, -1 = empty slot; an
  *        entry appears at most once per row; blocks after the row's own and
  *        blocks whose page is outside the pool contribute nothing; an entry
- *        outside [-1, max_pages) is ignored and recorded as MSA_DEV_BAD_INDEX
+ *        outside [-1, max_pages) is ignored and recorded as MSA_DEV_BAD_INDEX;
+ *        entries of skipped rows are not read
  *   o    [T, H_q, d_h] bf16, written (rounded once from fp32)
  *   lse  [T, H_q] fp32 natural-log LSE of the scaled logits, or NULL
  * A row whose selection leaves no key gets o = 0 and lse = -inf.  What lies in
