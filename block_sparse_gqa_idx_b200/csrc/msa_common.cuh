@@ -25,15 +25,20 @@ enum DevError : int {
 };
 
 struct DevStatus {
-  int code;   // first error seen (0 = none)
+  int code;   // first error seen (0 = none), or DEV_ERR_TIMEOUT
   int where;  // kernel-specific location tag
   int info0;
   int info1;
 };
 
+// The first error stays, but a timeout takes its place: after one the outputs
+// are invalid, while the other errors say that an entry or a sequence was left
+// out.
 MSA_DEVI void report(DevStatus* st, int code, int where, int a = 0, int b = 0) {
   if (st == nullptr) return;
-  if (atomicCAS(&st->code, 0, code) == 0) {
+  const bool first = code == DEV_ERR_TIMEOUT ? atomicExch(&st->code, code) != code
+                                             : atomicCAS(&st->code, 0, code) == 0;
+  if (first) {
     st->where = where;
     st->info0 = a;
     st->info1 = b;

@@ -512,7 +512,9 @@ MSA_API msa_status msa_paged_chunk_fp8(const msa_chunk_dims* dims, const void* q
 #define MSA_DEV_CAPACITY 4   /* an internal list overflowed its reservation */
 
 /* Synchronises `stream`, then copies the status word of `workspace` (written
- * by the last call that used it) into *code (and *where, if not NULL).
+ * by the last call that used it: the first error that the call met, or
+ * MSA_DEV_TIMEOUT if it met that one, whichever came first) into *code (and
+ * *where, if not NULL).
  * Returns MSA_ERR_DEVICE if *code != 0, MSA_OK otherwise. */
 MSA_API msa_status msa_get_device_status(const void* workspace, void* stream, int32_t* code,
                                  int32_t* where);

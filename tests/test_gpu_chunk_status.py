@@ -2,6 +2,8 @@
 of it: rows that a call skips have no entries to report."""
 from __future__ import annotations
 
+import time
+
 import pytest
 import torch
 
@@ -77,3 +79,22 @@ def test_step_with_padding_records_nothing(msa, new, have, wide):
     assert msa.device_status(ws) == (0, 0)
     live = (c.positions() >= 0).cuda()
     assert bool((idx[~live] == -9).all()) and bool((idx[live] >= -1).all())
+
+
+def test_a_timeout_takes_the_place_of_another_error(msa):
+    """An ignored entry, recorded first, does not hide that a wait gave up: outputs are invalid then.
+    (The entry's code is written here while the self-test's wait is running.)"""
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    word = ws.view(torch.int32)
+    bad_index = torch.tensor([2, 141], dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    waits, other = torch.cuda.Stream(), torch.cuda.Stream()
+    begun = torch.cuda.Event()
+    msa.selftest_bounded_wait(ws, stream=waits)
+    time.sleep(0.3)  # of the wait's two seconds
+    with torch.cuda.stream(other):
+        word[:2].copy_(bad_index)
+        begun.record()
+    begun.synchronize()
+    assert not waits.query()  # the wait was still running
+    assert msa.device_status(ws, stream=waits) == (1, 99)
