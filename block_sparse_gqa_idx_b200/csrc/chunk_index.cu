@@ -325,7 +325,7 @@ struct TcShape {
   static constexpr int OUT = kFlush * BPT + 1;      // maxima per row (padded)
   static constexpr size_t SMEM = 1024 + 2 * 2 * A_BYTES + ST * (K_BYTES + kKeys * 4) +
                                  2 * kRows * OUT * 4 + 4 * kRows * 4 + ST * 4 +
-                                 (2 * ST + 8) * 8 + 64 + (kTcThreads + 1) * 8;
+                                 (2 * ST + 9) * 8 + 64 + (kTcThreads + 1) * 8;
   static_assert(SMEM <= 227 * 1024, "shared memory of one CTA");
 };
 
@@ -415,7 +415,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   uint64_t* a_empty = a_full + 2;      // [2] MMAs done and row factors read
   uint64_t* acc_full = a_empty + 2;    // [2]
   uint64_t* acc_empty = acc_full + 2;  // [2]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
+  uint64_t* fin = acc_empty + 2;       // every MMA of the CTA finished
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(fin + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int64_t* pre = reinterpret_cast<int64_t*>(tmem_slot + 2);  // [threads + 1]
   const ChunkSeqs& c = p.c;
@@ -432,6 +433,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       mbar_init(&acc_full[j], 1);
       mbar_init(&acc_empty[j], 4);
     }
+    mbar_init(fin, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -528,9 +530,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
         umma_commit(&a_empty[ab]);
       }
-      // the commits have arrived before the CTA ends
-      for (uint32_t j = ua > 2 ? ua - 2 : 0; ok && j < ua; ++j)
-        ok = mbar_wait(&a_empty[j & 1], (j >> 1) & 1, abort_flag, p.status, 213);
+      // every MMA is done before TMEM is released, and every commit has arrived
+      // before the CTA ends, after a wait that gave up too
+      umma_commit(fin);
+      mbar_wait(fin, 0, nullptr, p.status, 213);
     }
   } else if (warp >= 4 && warp < 8) {
     // ---------------------------------------------------------- queries --
@@ -704,7 +707,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
   }
 
-  // every MMA is done once the epilogue has read its accumulators
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
