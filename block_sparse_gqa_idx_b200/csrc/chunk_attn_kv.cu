@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (int gen = 0; ok; ++gen) {
       const int slot = gen % kNKV;
-      if (!mbar_wait(&sc_full[slot], (gen / kNKV) & 1, abort_flag, p.status, 151)) break;
+      if (!mbar_wait_warp(&sc_full[slot], (gen / kNKV) & 1, abort_flag, p.status, 151)) break;
       const int keys = gen_keys[slot];
       if (keys == 0) break;  // no more generations
       uint8_t* sK = sKV + slot * SH::KV_BYTES;
@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
       for (int c = 0; ok && c < 2 * SH::CPP; ++c, ++ring) {
         const int rs = ring % kRaw;
-        ok = mbar_wait(&raw_full[rs], (ring / kRaw) & 1, abort_flag, p.status, 153);
+        ok = mbar_wait_warp(&raw_full[rs], (ring / kRaw) & 1, abort_flag, p.status, 153);
         if (!ok) break;
         const uint8_t* src = sRaw + rs * SH::RAW_BYTES + tid * 16;
         uint4 w[SH::NP];
@@ -325,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const int is = n % kIR, qs = n % QS;
         const int i = p.q0 + static_cast<int>(myslot / per_q);
-        if (!mbar_wait(&i_empty[is], ((n / kIR) & 1) ^ 1, abort_flag, p.status, 150)) break;
+        if (!mbar_wait_warp(&i_empty[is], ((n / kIR) & 1) ^ 1, abort_flag, p.status, 150)) break;
         TileInfo& ti = info[is];
         if (lane < len) {
           ti.slot[lane] = myslot;
@@ -339,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&i_full[is]);
-        if (!mbar_wait(&q_empty[qs], ((n / QS) & 1) ^ 1, abort_flag, p.status, 152)) break;
+        if (!mbar_wait_warp(&q_empty[qs], ((n / QS) & 1) ^ 1, abort_flag, p.status, 152)) break;
         if (lane == 0) mbar_arrive_expect_tx(&q_full[qs], len * p.R * D_H * 2);
         __syncwarp();
         const int h0 = p.G >= 8 ? r * p.G : (r * p.G / 8) * 8;
@@ -413,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int gen = 0;; ++gen) {
         const int slot = gen % kNKV;
         if (gen >= kNKV &&
-            !mbar_wait(&kv_empty[slot], ((gen / kNKV) - 1) & 1, abort_flag, p.status, 155))
+            !mbar_wait_warp(&kv_empty[slot], ((gen / kNKV) - 1) & 1, abort_flag, p.status, 155))
           break;
         // Value scales within kEven of one another (the usual page) are
         // stored relative to the largest: the softmax's weights times them
@@ -529,8 +529,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int hrow = row - q_local * p.R;
     for (int n = 0; n < my_tiles; ++n) {
       const int is = n % kIR;
-      if (!mbar_wait(&i_full[is], (n / kIR) & 1, abort_flag, p.status, 170)) break;
-      if (!mbar_wait(&o_full[n % kNS], (n / kNS) & 1, abort_flag, p.status, 171)) break;
+      if (!mbar_wait_warp(&i_full[is], (n / kIR) & 1, abort_flag, p.status, 170)) break;
+      if (!mbar_wait_warp(&o_full[n % kNS], (n / kNS) & 1, abort_flag, p.status, 171)) break;
       tc_fence_after();
       const TileInfo& ti = info[is];
       const int goff = p.G >= 8 ? 0 : (ti.r * p.G) % 8;  // group's first head in the box
@@ -588,7 +588,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int qA = rowA / p.R, qB = rowB / p.R;
     for (int n = team; n < my_tiles; n += 2) {
       const int is = n % kIR, st = n % kNS;
-      if (!mbar_wait(&i_full[is], (n / kIR) & 1, abort_flag, p.status, 180)) break;
+      if (!mbar_wait_warp(&i_full[is], (n / kIR) & 1, abort_flag, p.status, 180)) break;
       const TileInfo& ti = info[is];
       const int jb = ti.jb + 2 * cq;
       const int iA = qA < ti.len ? ti.qi[qA] - jb : INT_MAX, iB = qB < ti.len ? ti.qi[qB] - jb : INT_MAX;
@@ -596,7 +596,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool cut = __any_sync(0xFFFFFFFFu, (iA < iB ? iA : iB) < B_K);
       // page scales: they stay until the page's last O = P V is done
       const float* sc = sSc + (ti.gen % kNKV) * SH::SCALES_PAD;
-      if (!mbar_wait(&s_full[st], (n / kNS) & 1, abort_flag, p.status, 181)) break;
+      if (!mbar_wait_warp(&s_full[st], (n / kNS) & 1, abort_flag, p.status, 181)) break;
       tc_fence_after();
       const uint32_t tS = tmem_base + st * 128 + SH::TM_S + (static_cast<uint32_t>(lane0) << 16);
       const float unit = sc[2 * B_K];

@@ -474,8 +474,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             have |= pg[j] >= 0 ? 1 << j : 0;
           }
           const int st = g % ST;
-          ok = mbar_wait(&k_empty[st], ((g / ST) & 1) ^ 1, abort_flag, p.status, 200);
-          ok = __all_sync(0xFFFFFFFFu, ok);
+          ok = mbar_wait_warp(&k_empty[st], ((g / ST) & 1) ^ 1, abort_flag, p.status, 200);
           if (!ok) break;
           if (lane == 0) {
             sOk[st] = have;
@@ -544,7 +543,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     for (int64_t u = blockIdx.x; u < plan.units; u += gridDim.x, ++ua) {
       const int ab = ua & 1;
       const TcUnit it = plan.unit(u);
-      if (!mbar_wait(&a_empty[ab], ((ua >> 1) & 1) ^ 1, abort_flag, p.status, 220)) break;
+      if (!mbar_wait_warp(&a_empty[ab], ((ua >> 1) & 1) ^ 1, abort_flag, p.status, 220)) break;
       uint8_t* hi = sA + ab * 2 * SH::A_BYTES;
       constexpr int NP = 4;  // passes whose rows are loaded together
 #pragma unroll 1
@@ -622,7 +621,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     for (int64_t u = blockIdx.x; u < plan.units; u += gridDim.x, ++ua) {
       const int ab = ua & 1;
       const TcUnit it = plan.unit(u);
-      ok = ok && mbar_wait(&a_full[ab], (ua >> 1) & 1, abort_flag, p.status, 230);
+      ok = ok && mbar_wait_warp(&a_full[ab], (ua >> 1) & 1, abort_flag, p.status, 230);
       const float* row_f = sRow + ab * kRows;
       const int b_end = it.b_end;
       float* out_g = p.out + it.row0 * max_pages;
@@ -648,9 +647,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         for (int kt = it.k0; kt < it.k1; ++kt, ++g) {
           if ((g & 1) != grp) continue;
           const int st = g % ST;
-          ok = ok && mbar_wait(&k_full[st], (g / ST) & 1, abort_flag, p.status, 231) &&
-               mbar_wait(&acc_full[grp], (g >> 1) & 1, abort_flag, p.status, 232);
-          ok = __all_sync(0xFFFFFFFFu, ok);
+          ok = ok && mbar_wait_warp(&k_full[st], (g / ST) & 1, abort_flag, p.status, 231) &&
+               mbar_wait_warp(&acc_full[grp], (g >> 1) & 1, abort_flag, p.status, 232);
           tc_fence_after();
           const uint32_t ta = tmem_base + grp * 256 + (static_cast<uint32_t>(quarter * 32) << 16);
           const float* sc = sS + st * kKeys;

@@ -114,6 +114,14 @@ MSA_DEVI bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* abort, Dev
   }
 }
 
+// The same by a whole warp, which goes one way: the lanes see the barrier and the
+// abort flag at different times, and what follows needs all of them (shuffles,
+// votes, TMEM accesses).
+MSA_DEVI bool mbar_wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort, DevStatus* st,
+                             int where) {
+  return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort, st, where));
+}
+
 // -------------------------------------------------------------- mma.sync --
 // D (16x8, f32) += A (16x16, bf16, row) * B (16x8, bf16, col).  Thread
 // (g = lane/4, t = lane%4) holds A rows g and g+8 at k = 2t, 2t+1 (+8), B
