@@ -742,9 +742,18 @@ def _theta_freqs(rot_dim: int, theta: float):
     return (ctypes.c_double * max(n, 1))(*[theta ** (-2.0 * j / rot_dim) for j in range(n)])
 
 
+def _filled(struct, values):
+    """struct(*values), refusing integers that their fields would cut (ctypes keeps the low bits)."""
+    d = struct(*values)
+    for (name, kind), v in zip(struct._fields_, values):
+        if kind is not ctypes.c_float and getattr(d, name) != v:
+            raise ValueError(f"{name} = {v} is out of range")
+    return d
+
+
 @functools.lru_cache(maxsize=256)
 def _norm_rope_dims(*sizes):
-    d = msa_norm_rope_dims(*sizes)
+    d = _filled(msa_norm_rope_dims, sizes)
     return d, ctypes.byref(d)
 
 
@@ -838,9 +847,9 @@ def qk_norm_rope_bwd(q: torch.Tensor, k: torch.Tensor, w_q: Optional[torch.Tenso
 
 def chunk_dims(S, T, max_pages, n_pages, H_q, H_kv, d_h, d_idx, B_k, k, attn_scale=0.0,
                idx_scale=0.0) -> msa_chunk_dims:
-    return msa_chunk_dims(int(S), int(T), int(max_pages), int(n_pages), int(H_q), int(H_kv),
-                          int(d_h), int(d_idx), int(B_k), int(k), float(attn_scale),
-                          float(idx_scale))
+    return _filled(msa_chunk_dims, (int(S), int(T), int(max_pages), int(n_pages), int(H_q), int(H_kv),
+                                    int(d_h), int(d_idx), int(B_k), int(k), float(attn_scale),
+                                    float(idx_scale)))
 
 
 @functools.lru_cache(maxsize=1024)
