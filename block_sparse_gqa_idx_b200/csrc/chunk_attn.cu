@@ -579,18 +579,32 @@ cudaError_t launch_direct(const AttendLaunch& a, cudaStream_t s) {
 }  // namespace
 
 // Which form.  The query-outer kernel's time is the bytes of the selected pages as
-// every row reads them (through L2); the KV-outer form costs about 30 us of short
-// kernels and each page once, and pays from about 2^28 such values on (H_q = 32,
-// H_kv = 4, d_h = B_k = 128, k = 16: 256 rows).  Measured there, query-outer against
-// KV-outer, one sequence at 9K / four at 9K / one at 61K: 128 rows 53 : 46 / 54 : 56 /
-// 54 : 83 us, 256 rows 93 : 51 / 95 : 74 / 95 : 87, 512 rows 151 : 76 / 153 : 107 /
-// 152 : 127; H_q = 8, H_kv = 2, 256 rows 52 : 37 / 52 : 45 / 52 : 51; d_h = B_k = 64,
-// k = 8, 512 rows 40 : 44 / 40 : 60 / 41 : 93.
+// every row reads them (through L2).  The KV-outer form costs about 30 us of short
+// kernels, and a tile for each page and up to 16 of the rows that chose it (8 when
+// G = 16), full or not.  It pays from about 2^28 values on, and where sequences have
+// many rows, so that rows share pages: 24 on average, as far as the host knows.
+// Query-outer : KV-outer, us, with H_q = 32, H_kv = 4, d_h = B_k = 128, k = 16 unless
+// said, and selections scattered over the context but for its first and last blocks:
+//   size       one sequence at 9K / four at 9K / one at 61K: 128 rows 53 : 46 /
+//              54 : 56 / 54 : 83, 256 rows (2^28) 93 : 51 / 95 : 74 / 95 : 87, 512 rows
+//              151 : 76 / 153 : 107 / 152 : 127.  2^27 values are not enough: H_q = 8,
+//              H_kv = 2, 256 rows 52 : 38 / 53 : 48 / 52 : 52, but at 128K 57 : 79, and
+//              H_kv = 8, B_k = 64, k = 8, 256 rows at 9K / 61K 56 : 64 / 59 : 174.
+//              (G = 16, one sequence at 9K: 64, 128, 256 rows 38 : 44, 69 : 53, 120 : 80.)
+//   rows       single tokens of 64, 256, 512 sequences 45 : 188, 123 : 574, 195 : 1088.
+//              64 chunks of 16, 24, 32 rows 296 : 461, 437 : 512, 578 : 543; one long
+//              chunk beside 63 single tokens, as many rows 297 : 277, 437 : 314, 577 : 362.
+//   context    one sequence at 128K / 1M: 256 rows 96 : 154 / 112 : 379, 1024 rows
+//              293 : 220 / 331 : 775, 4096 rows 1190 : 462 / 1429 : 997.  Not in the rule:
+//              only the device knows it, and a table may be far wider than it.
+//   table      four sequences of 128 rows, 256, 1024, 8192 entries each: 152 : 87, 97, 106.
+constexpr int64_t kShareRows = 24;
 static bool kv_outer(const msa::ChunkSeqs& c, int H_q, int H_kv, int d_h, int k) {
   const int G = H_q / H_kv;
   if (16 % G != 0 || (G < 8 && H_q % 8 != 0)) return false;  // its MMA rows and TMA boxes
   if (static_cast<int64_t>(c.S) * c.max_pages * H_kv >= (int64_t(1) << 30)) return false;  // keys
   if (c.n_pages * c.B_k >= (int64_t(1) << 31)) return false;  // TMA row coordinates
+  if (c.T < kShareRows * c.S) return false;
   return static_cast<int64_t>(c.T) * H_kv * k * c.B_k * d_h >= (int64_t(1) << 28);
 }
 
