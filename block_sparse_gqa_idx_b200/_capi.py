@@ -797,7 +797,8 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, w_q: Optional[torch.Tensor],
     (j, j + rot_dim/2), or (2j, 2j + 1) when interleaved, turn by
     pos * inv_freq[j] (theta^(-2j/rot_dim) unless given); the rest passes
     through.  Rows with pos < 0 are left as they were in q_out and k_out, which
-    may be q and k themselves.  Returns (q_out, k_out)."""
+    may be q and k themselves.  The mean of squares is held in fp32: magnitudes up
+    to about 1e18, and no row of zeros where eps is 0.  Returns (q_out, k_out)."""
     device, sizes, freqs = _norm_rope_args(q, k, w_q, w_k, pos, rot_dim, theta, eps, interleaved,
                                            inv_freq)
     with _on(device, stream):

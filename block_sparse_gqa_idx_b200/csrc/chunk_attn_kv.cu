@@ -23,8 +23,8 @@
 // partial stays within 128 * 448 < 65504.
 //
 // 4096 rows of two sequences at 61K cached tokens (H_q = 32, H_kv = 4, d_h =
-// B_k = 128, k = 16; 137 GFLOP): 349 us in the tile kernel, of 458 in all (the
-// query-outer kernel: 1406); the merge reads its 537 MB of partials in 88.
+// B_k = 128, k = 16; 137 GFLOP): 355 us in the tile kernel, of 465 in all (the
+// query-outer kernel: 1122); the merge reads its 537 MB of partials in 88.
 // What bounds the tiles is the MMAs beside the softmax's TMEM reads: S and O
 // take 1200 and 1500 clocks a tile in place, 512 each at the peak rate.
 #include <climits>
@@ -579,8 +579,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // for the weights, 32 keys ahead: the loops are short, so that the teams'
     // code stays in the instruction caches, and 72 registers are enough for
     // 16 warps (straight-line code over a row's keys with half the warps: 410
-    // us on 18000 tiles, this 349; there ncu counts 4.4 warps per issue that
-    // wait for instructions, here 1.1).
+    // us on 18000 tiles, this 349 when they were compared; there ncu counts 4.4
+    // warps per issue that wait for instructions, here 1.1).
     const int team = (warp - 8) >> 3;
     const int lane0 = (warp & 3) * 32 + ((warp >> 2) & 1) * 16;
     const int cq = lane & 3;

@@ -14,10 +14,12 @@
 // Two forms, each with its own sequences of a batch (see kTcRows).  For single
 // tokens the bound is the cache's bytes: 32 x 32.7K keys, d_idx = 64 (71 MB),
 // 18.5 us, 3.8 TB/s; the rest is the launch, the look-ups and the last blocks of
-// warps that have one more than others.  For long chunks it is what the epilogue
-// does with the products, a multiplication by the key's scale and a maximum for
-// each: 4096 tokens of four groups x 61K keys take 236 us, 0.48 PFLOP/s (the
-// tensor cores do twice that: two terms per query).
+// warps that have one more than others.  For long chunks it is latency: 4096 tokens
+// of four groups x 61K keys take 232 us, 0.49 PFLOP/s (the tensor cores do twice
+// that: two terms per query), with the tensor pipe at 27 to 31 %, the issue slots at
+// 36 % and the shared-memory pipe at 51 % of their peaks.  The eight epilogue warps
+// mostly wait: for each 32 columns of TMEM in turn (40 % of all stalled cycles),
+// and at their groups' barriers around the writing of the maxima (20 %).
 #include <cuda_fp8.h>
 
 #include <climits>

@@ -5,12 +5,17 @@
 //           x / scale, to nearest even: the rule of the decode step's append
 //   gather  bf16 of code * scale
 //
-// Both are bound by the bytes they move.  A CTA takes a few consecutive tokens:
-// their pages are looked up once, by one thread each, and then all threads walk
-// the tokens' K, V and index-key rows in 16-code pieces (16 bytes of codes, 32 of
-// bf16), several in flight per thread.  A row's maximum is a shuffle reduction
-// over the d/16 lanes that hold it.  65536 tokens read back (H_kv = 4, d_h =
-// 128, d_idx = 64; 217 MB): 43 us, 5.0 TB/s.  8192 appended (27 MB): 14.4 us; a
+// A CTA takes a few consecutive tokens: their pages are looked up once, by one
+// thread each, and then all threads walk the tokens' rows in 16-code pieces (16
+// bytes of codes, 32 of bf16): the gather's all three tensors' and two pieces at a
+// time, the append's one tensor's (the grid's second axis) and one piece at a time.
+// A row's maximum is a shuffle reduction over the d/16 lanes that hold it.
+// The gather is bound by its bytes: 65536 tokens (H_kv = 4, d_h = 128, d_idx = 64;
+// 217 MB) 43 us, 5.0 TB/s.  The append is not: 8192 tokens (27 MB) take 14.4 us, 1.9
+// TB/s, 3.5 times their bytes.  Its instructions keep 57 % of the issue slots busy
+// (a piece has 16 exact quotients and their conversions; the conversion pipe is at
+// 47 %), each CTA begins with the look-ups, a chain of dependent loads, with
+// nothing else in flight, and 1536 CTAs are 1.7 rounds of what the SMs hold.  A
 // launch of few bytes is the latency of its look-ups, 4 us for 128 tokens.
 #include <cuda_fp8.h>
 

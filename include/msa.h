@@ -348,7 +348,10 @@ MSA_API msa_status msa_quantize_fp8_rows(const void* x, int64_t n_rows, int32_t 
  *   n = x / sqrt(mean over the head of x^2 + eps),  y = R(pos) (w * n)
  * R rotates the pairs (j, j + rot/2), or (2j, 2j + 1) when interleaved, by the
  * angle pos * inv_freq[j], j < rot/2; dimensions rot .. d-1 pass through.
- * Angles are exact at any int32 position (64-bit fixed point turns).
+ * Angles are exact at any int32 position (64-bit fixed point turns).  The mean of
+ * squares is held in fp32, whose range it must not leave: rows of magnitudes up to
+ * about 1e18 and, where eps is 0, not below 1e-18 (nor rows of zeros, which have no
+ * norm then: NaN).
  *   q [T, H_q, d], k [T, H_k, d] bf16      w_q, w_k [d] bf16 or NULL (ones)
  *   pos       [T] int32; a row with pos < 0 is padding: its outputs are left
  *             as they were, its gradients are zero and it adds nothing to dw

@@ -40,3 +40,29 @@ def test_norm_rope_sizes_that_do_not_fit(capi, at):
     sizes[at] += 2**32
     with pytest.raises(ValueError):
         capi._norm_rope_dims(*sizes)
+
+
+def test_host_tensors_are_refused(capi):
+    """As by every entry point: there is no other implementation to fall back to."""
+    import torch
+
+    T, S, P, B, H, d, di = 4, 2, 6, 64, 2, 64, 64
+    bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16)  # noqa: E731
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    u8 = lambda *s: torch.zeros(s, dtype=torch.uint8)  # noqa: E731
+    pages = [u8(P, B, H, d), torch.zeros(P, B, H), u8(P, B, H, d), torch.zeros(P, B, H)]
+    pools = [*pages, u8(P, B, di), torch.zeros(P, B)]
+    seqs = [i32(S, 3), i32(S + 1), i32(S)]
+    q, k, qi, ki = bf(T, 2 * H, d), bf(T, H, d), bf(T, H, di), bf(T, di)
+    w = bf(d)
+    for call in (lambda: capi.qk_norm_rope(q, k, w, w, i32(T)),
+                 lambda: capi.qk_norm_rope_bwd(q, k, w, w, i32(T), q, k),
+                 lambda: capi.chunk_positions(seqs[1], seqs[2], T),
+                 lambda: capi.paged_append_fp8(k, k, ki, *pools, *seqs),
+                 lambda: capi.paged_gather_fp8(*pools, *seqs, T),
+                 lambda: capi.paged_index_scores_fp8(qi, *pools[4:], *seqs),
+                 lambda: capi.block_topk(torch.zeros(T, H, 3), i32(T), B, 2),
+                 lambda: capi.paged_sparse_attn_fp8(q, i32(T, H, 2), *pages, *seqs),
+                 lambda: capi.paged_chunk_fp8(q, qi, k, k, ki, *pools, *seqs, 2)):
+        with pytest.raises(ValueError, match="CUDA"):
+            call()
