@@ -48,6 +48,8 @@ CASES = [  # new, have, B_k, H_kv, G, d_h, k, pad
     ([257], [10], 64, 4, 8, 64, 4, 5),
     ([300, 20], [500, 300], 128, 2, 8, 128, 5, 2),
     # enough rows x selected keys for the KV-outer form
+    # (meant to be; some are too small for it, or have too few rows a sequence: which form a
+    # case takes is asserted in test_gpu_chunk_forms.py)
     ([300, 20], [500, 300], 128, 4, 8, 128, 8, 2),
     ([530], [10], 64, 8, 1, 64, 8, 0),
     ([257, 0, 9], [1000, 5, 64], 128, 4, 16, 64, 16, 3),
@@ -59,6 +61,7 @@ CASES = [  # new, have, B_k, H_kv, G, d_h, k, pad
     ([1030, 0, 9], [1000, 5, 64], 64, 4, 16, 64, 16, 3),
     ([1] * 90 + [130] * 5, [130] * 95, 128, 4, 8, 128, 6, 0),
     # every number of heads per group with either head size
+    # (16 heads with d_h = 128: test_gpu_chunk_forms.py)
     ([1030], [10], 64, 8, 1, 128, 8, 2),
     ([1100, 3], [10, 700], 64, 8, 2, 64, 8, 0),
     ([600], [500], 128, 4, 4, 64, 16, 1),

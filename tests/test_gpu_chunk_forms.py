@@ -64,3 +64,28 @@ def test_form_and_result(msa, form, new, have, B_k, H_kv, G, d_h, k, pad):
     none = rl == -float("inf")
     assert torch.equal(lse == -float("inf"), none) and bool((o[none] == 0).all())
     assert bool(((o - ro).abs() <= otol)[~none].all()) and bool(((lse - rl).abs() <= ltol)[~none].all())
+
+
+@pytest.mark.parametrize("wide", [4200, 9000])
+def test_wide_tables_of_many_rows(msa, wide):
+    """Page tables of more (group, block) pairs than one CTA scans (33600), and than a CTA counts in shared
+    memory (72000): the KV-outer form gives what it gives with a narrow table, bit for bit."""
+    c = Cache([700, 30], [500, 64], 64, 4, 128, 64, seed=93, wide=wide)
+    q = torch.randn(c.T, 32, 128, generator=c.g).bfloat16()
+    idx = selection(c, 16, holes=True)
+    d = c.gpu(c.appended())
+    narrow = d["table"][:, :24].contiguous()
+    got = []
+    for table in (d["table"], narrow):
+        msa.profile_enable(True)
+        try:
+            got.append(msa.paged_sparse_attn_fp8(q.cuda(), idx.cuda(), *c.pools(d)[:4], table, d["cu"], d["len"]))
+            ran = set(msa.profile_read())
+        finally:
+            msa.profile_enable(False)
+        assert "chunk_tile" in ran and ("inv_count" in ran) == (table is not narrow)
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+    o, lse = (t.double().cpu() for t in got[0])
+    ro, rl, otol, ltol = attention(c, q, idx, 128**-0.5)
+    none = rl == -float("inf")
+    assert bool(((o - ro).abs() <= otol)[~none].all()) and bool(((lse - rl).abs() <= ltol)[~none].all())
