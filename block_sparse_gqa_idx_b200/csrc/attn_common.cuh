@@ -31,8 +31,6 @@ constexpr int kWindow = kMaxChunk;
 // 128-byte swizzle atom) when G < 8 (the extra heads are computed and dropped).
 inline int rows_per_query(int G) { return G >= 8 ? G : 8; }
 
-inline size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
-
 struct ChunkBufs {
   int32_t* counts;    // [nkeys]
   int32_t* offsets;   // [nkeys + 1]

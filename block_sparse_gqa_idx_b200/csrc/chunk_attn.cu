@@ -27,8 +27,6 @@
 //     by more than 2^10, so a step costs one vote instead of two reductions.
 // Single tokens of 48 sequences at 16K (H_q = 32, H_kv = 4, d_h = B_k = 128, k = 16;
 // 104 MB): 28 us, and 4 for the join of two splits; 3.7 TB/s.
-#include <cuda_fp8.h>
-
 #include "chunk_launch.h"
 
 namespace msa {
@@ -56,11 +54,6 @@ struct AttendParams {
   DevStatus* status;
 };
 
-__device__ __forceinline__ uint32_t widen2(uint32_t c2) {
-  const __half2_raw h =
-      __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(c2 & 0xFFFFu), __NV_E4M3);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
 __device__ __forceinline__ uint32_t pack_f16(float a, float b) {
   const __half2 h = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -525,8 +518,6 @@ int splits_of(int T, int H_q, int H_kv, int B_k, int d_h, int k) {
   }
   return best;
 }
-
-size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 template <int D, int BK, int NH>
 cudaError_t launch_attend(const AttendParams& p, unsigned grid, cudaStream_t s) {

@@ -96,13 +96,8 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, int a_mn, int
          (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
-__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t c2) {
-  const __half2_raw h =
-      __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(c2 & 0xFFFFu), __NV_E4M3);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
 __device__ __forceinline__ uint32_t e4m3x2_bf16x2(uint32_t c2) {
-  const uint32_t h = e4m3x2_f16x2(c2);
+  const uint32_t h = widen2(c2);
   const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
   return pack_bf16(f.x, f.y);
 }
@@ -287,11 +282,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               sc[B_K + key] = __int_as_float(0x7FC00000);
             }
             put(sK + SH::K_BYTES, key, 0,
-                make_uint4(e4m3x2_f16x2(x.x), e4m3x2_f16x2(x.x >> 16), e4m3x2_f16x2(x.y),
-                           e4m3x2_f16x2(x.y >> 16)));
+                make_uint4(widen2(x.x), widen2(x.x >> 16), widen2(x.y),
+                           widen2(x.y >> 16)));
             put(sK + SH::K_BYTES, key, 1,
-                make_uint4(e4m3x2_f16x2(x.z), e4m3x2_f16x2(x.z >> 16), e4m3x2_f16x2(x.w),
-                           e4m3x2_f16x2(x.w >> 16)));
+                make_uint4(widen2(x.z), widen2(x.z >> 16), widen2(x.w),
+                           widen2(x.w >> 16)));
           }
         }
       }

@@ -86,12 +86,10 @@ msa::NormRopeLaunch norm_rope_launch(const msa_norm_rope_dims* d, const double* 
   return a;
 }
 
-size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
-
 size_t scores_bytes(const msa_chunk_dims* d) {
-  return align256(sizeof(float) * static_cast<size_t>(d->T) * d->H_kv * d->max_pages);
+  return msa::align256(sizeof(float) * static_cast<size_t>(d->T) * d->H_kv * d->max_pages);
 }
-size_t pos_bytes(const msa_chunk_dims* d) { return align256(sizeof(int32_t) * d->T); }
+size_t pos_bytes(const msa_chunk_dims* d) { return msa::align256(sizeof(int32_t) * d->T); }
 
 }  // namespace
 

@@ -8,12 +8,21 @@
 // kernels, never trusted: a row that no sequence holds, or whose sequence
 // does not fit max_pages * B_k tokens, has position -1 and is skipped.
 #pragma once
+#include <cuda_fp8.h>
+
 #include "msa_internal.h"
 
 namespace msa {
 
 // 2^e, -126 <= e <= 127.
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
+
+// Two E4M3 codes -> an f16 pair (exact), one conversion instruction.
+__device__ __forceinline__ uint32_t widen2(uint32_t c2) {
+  const __half2_raw h =
+      __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(c2 & 0xFFFFu), __NV_E4M3);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
 
 struct ChunkSeqs {
   const int32_t* cu;       // [S + 1]

@@ -122,13 +122,6 @@ __device__ __forceinline__ int seq_find(int S, const int64_t* pre, int64_t& u, F
   return s;
 }
 
-// Two E4M3 codes -> an f16 pair (exact), one conversion instruction.
-__device__ __forceinline__ uint32_t widen2(uint32_t c2) {
-  const __half2_raw h =
-      __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(c2 & 0xFFFFu), __NV_E4M3);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-
 // Scores on mma.sync, straight from global memory, for sequences with few rows.
 // MMA rows = 16 keys, whose codes widen to f16 in registers; columns = the
 // (token, group) rows of one sequence's tokens, NT tiles of 8.  The d axis is

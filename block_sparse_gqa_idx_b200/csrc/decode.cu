@@ -28,8 +28,6 @@
 namespace msa {
 namespace {
 
-size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
-
 struct DecBufs {
   int32_t* Lcur;    // [S] this step's length before the append, -1 = skipped
   float* M;         // [S, H_kv, Bmax] block maxima (raw dots)

@@ -467,7 +467,7 @@ msa_status check_attn_varlen(const msa_varlen_dims* d, const int64_t* cu) {
   return check_attn_dims(&f);
 }
 
-size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+using msa::align256;
 
 }  // namespace
 

@@ -25,6 +25,8 @@ bool make_tmap_bf16(CUtensorMap* map, const void* base, int rank, const uint64_t
 
 int num_sms();
 
+inline size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+
 // Launch `kern` so that it may start while the previous kernel of the stream
 // finishes (programmatic stream serialization); the kernel must call
 // griddep_wait() before it reads anything the previous kernel writes.

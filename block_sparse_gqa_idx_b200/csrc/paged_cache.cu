@@ -17,10 +17,6 @@
 // 47 %), each CTA begins with the look-ups, a chain of dependent loads, with
 // nothing else in flight, and 1536 CTAs are 1.7 rounds of what the SMs hold.  A
 // launch of few bytes is the latency of its look-ups, 4 us for 128 tokens.
-#include <cuda_fp8.h>
-
-#include "chunk_common.cuh"
-
 #include "chunk_launch.h"
 
 namespace msa {
@@ -154,8 +150,7 @@ __global__ void __launch_bounds__(kThreads) paged_gather_kernel(const CacheParam
       uint32_t out[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
-            static_cast<__nv_fp8x2_storage_t>((in[e >> 1] >> (16 * (e & 1))) & 0xFFFFu), __NV_E4M3);
+        const uint32_t h = widen2(in[e >> 1] >> (16 * (e & 1)));
         const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
         out[e] = pack_bf16(f.x * sc[j], f.y * sc[j]);
       }

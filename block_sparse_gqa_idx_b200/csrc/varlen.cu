@@ -26,8 +26,6 @@ namespace {
 
 constexpr int kTileRows = 128;  // Q_idx rows of the index kernel's M-tile
 
-size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
-
 struct Counts {
   int64_t B_tot = 0;
   int64_t n_tiles = 0;
