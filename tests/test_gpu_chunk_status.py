@@ -89,12 +89,14 @@ def test_a_timeout_takes_the_place_of_another_error(msa):
     bad_index = torch.tensor([2, 141], dtype=torch.int32, device="cuda")
     torch.cuda.synchronize()
     waits, other = torch.cuda.Stream(), torch.cuda.Stream()
-    begun = torch.cuda.Event()
-    msa.selftest_bounded_wait(ws, stream=waits)
-    time.sleep(0.3)  # of the wait's two seconds
-    with torch.cuda.stream(other):
-        word[:2].copy_(bad_index)
-        begun.record()
-    begun.synchronize()
-    assert not waits.query()  # the wait was still running
-    assert msa.device_status(ws, stream=waits) == (1, 99)
+    for _ in range(3):  # again where the host was held up for longer than the wait
+        msa.selftest_bounded_wait(ws, stream=waits)
+        time.sleep(0.3)  # of the wait's two seconds
+        with torch.cuda.stream(other):
+            word[:2].copy_(bad_index)
+        other.synchronize()
+        running = not waits.query()
+        status = msa.device_status(ws, stream=waits)
+        if running:
+            break
+    assert running and status == (1, 99)
